@@ -20,6 +20,13 @@
  *   bgtq_logit_mae      per-layer logit error of the packed keys (diagnostic)
  *   bgtq_set_block_table  page table of a paged cache
  *
+ * Beside the packed cache, an 8-bit one for layers that 4 bits do not hold:
+ *
+ *   bgtq_byte_append       e4m3 or int8 codes, one scale per 64 positions and head
+ *   bgtq_byte_decode_attn  attention over it for 1..16 tokens a sequence, with
+ *                          capped, distance-biased, windowed, prefix- and
+ *                          document-masked scores
+ *
  * Conventions
  *  - Every function returns 0 (BGTQ_OK) or a negative BGTQ_ERR_* code and
  *    never throws or aborts.  Argument checks happen before any launch; a
@@ -92,7 +99,8 @@ enum {
   BGTQ_DEVERR_SEQ_LEN = 2,     /* decode: a seq_len < 0 or > capacity (sequence skipped, output 0), or a pos_lo /
                                   buf_count out of range (clamped) */
   BGTQ_DEVERR_ARG = 4,         /* encode_append: start < 0 or count < 0 or count > n */
-  BGTQ_DEVERR_NONFINITE = 8,   /* allocate: a calibration value is Inf or NaN */
+  BGTQ_DEVERR_NONFINITE = 8,   /* allocate: a calibration value is Inf or NaN; byte_append: a row's element is
+                                  (stored as the largest code, NaN as 0) */
   BGTQ_DEVERR_TIMEOUT = 16,    /* decode: a wait for a tile copy gave up (bounded spin) */
   BGTQ_DEVERR_PAGE = 32        /* paged cache: a block-table entry outside [0, page_pool_tiles) (encode skips the
                                   tile, decode reads page 0 instead, logit MAE skips the tile) */
@@ -433,6 +441,114 @@ int bgtq_set_decode_path(bgtq_state* st, int32_t fused);
  * co-schedule its cluster for the config.  Both compute the same attention.
  * SYNC (host only; the first call may query the GPU's occupancy). */
 int bgtq_get_decode_path(bgtq_state* st, int32_t* h_fused, int32_t* h_ctas);
+
+/* ---- The 8-bit cache ---------------------------------------------------
+ *
+ * A cache of 8-bit codes beside the packed one: for layers, heads or models
+ * that 1..4 bits do not hold, with the packed cache's 64-position blocks,
+ * layouts, paging and call conventions.  No calibration, rotation or
+ * allocation comes before it.  A state made by bgtq_byte_create works with
+ * bgtq_destroy, bgtq_cache_offsets, bgtq_set_block_table,
+ * bgtq_test_drop_tile_copies, bgtq_get_device_error and the calls below; the
+ * packed cache's other calls answer BGTQ_ERR_NOT_READY or
+ * BGTQ_ERR_INVALID_ARG for it, and the bgtq_byte_* calls
+ * BGTQ_ERR_INVALID_ARG for a packed state.
+ *
+ * Arrays (bgtq_cache_offsets: K codes, K scales, V codes, V scales), with
+ * slots [L][B][H][T] contiguous or [L][H][P] paged as for the packed cache:
+ *   codes   uint8 [slots][64][128]  e4m3 (OCP, no infinities) or int8, row p
+ *                                   = position 64 t + p, plain order
+ *   scales  fp32 [slots]            a power of two, at least 2^-100
+ * The value of a code is code * scale.  One scale for the 64 positions of a
+ * (layer, sequence or page, KV head) block, K and V apart. */
+enum { BGTQ_CODE_E4M3 = 0, BGTQ_CODE_INT = 1 };       /* int: int8, -127 .. 127 */
+enum { BGTQ_DTYPE_HALF = 0, BGTQ_DTYPE_BFLOAT = 1 };  /* fp16, bf16 */
+
+typedef struct {
+  int32_t n_layers;          /* 1..65535 */
+  int32_t n_kv_heads;        /* >= 1 */
+  int32_t n_q_heads;         /* multiple of n_kv_heads; G = n_q_heads / n_kv_heads <= 16 */
+  int32_t head_dim;          /* must be 128 */
+  int32_t max_batch;         /* >= 1 */
+  int32_t code;              /* BGTQ_CODE_* */
+  int32_t dtype;             /* BGTQ_DTYPE_* of appended rows, queries and outputs */
+  int32_t max_q_tokens;      /* most query tokens of a sequence in one call, 1..16 */
+  int32_t page_pool_tiles;   /* 0: contiguous; > 0: paged, this many 64-position pages per (layer, KV head) */
+  int32_t reserved;          /* 0 */
+  int64_t capacity_tokens;   /* cached tokens per sequence, 1..2^30 */
+} bgtq_byte_config;
+
+/* Bytes of the two caller-owned device buffers.  A config of 2^31 - 64 or
+ * more positions over all layers, heads and sequences (or pages) is
+ * rejected with BGTQ_ERR_INVALID_ARG.  SYNC (host only). */
+int bgtq_byte_required_bytes(const bgtq_byte_config* cfg, size_t* cache_bytes, size_t* workspace_bytes);
+
+/* Creates a state over caller buffers (256-byte aligned, at least the
+ * required sizes; they must outlive it).  The cache's contents are left as
+ * they are: a zeroed buffer holds zeros.  SYNC. */
+int bgtq_byte_create(const bgtq_byte_config* cfg, void* d_cache, size_t cache_bytes, void* d_workspace,
+                     size_t workspace_bytes, void* stream, bgtq_state** out);
+
+/* Quantises and stores new rows: for each layer l in [layer, layer +
+ * layer_count), sequence b < batch, row r < count[b], the K and V rows go to
+ * position start[b] + r.  Per block, K and V apart: a = the largest finite
+ * magnitude of the call's rows in it, Qmax = 448 (e4m3) or 127 (int8), e_new
+ * = the least integer >= -100 with a <= Qmax 2^e_new.  A call that writes the
+ * block's first position starts the block anew: e = e_new, and its other
+ * positions keep bytes that mean nothing until they are written.  Otherwise e
+ * = max(e_old, e_new); where e grew, the block's other codes are rescaled
+ * (round(code 2^(e_old - e)), ties to even).  New codes are round(x 2^-e),
+ * ties to even; the scale is 2^e.  Infinities become the largest code and
+ * NaN 0, with BGTQ_DEVERR_NONFINITE.
+ *   d_k, d_v   fp16 or bf16 [layer_count][batch][n][n_kv_heads][128]
+ *   d_start    int32 [batch]
+ *   d_count    int32 [batch], 0..n
+ * Positions at or past the capacity are skipped and set
+ * BGTQ_DEVERR_CAPACITY; start < 0 or count outside 0..n skips the sequence
+ * and sets BGTQ_DEVERR_ARG; a page id outside the pool skips the block and
+ * sets BGTQ_DEVERR_PAGE.  Two sequences must not write one page.  One launch.
+ * ASYNC. */
+int bgtq_byte_append(bgtq_state* st, int32_t layer, int32_t layer_count, const void* d_k, const void* d_v,
+                     const int32_t* d_start, const int32_t* d_count, int32_t batch, int32_t n, void* stream);
+
+/* How bgtq_byte_decode_attn scores query i of sequence b, at position
+ * p = seq_lens[b] - n_q + i, against position t.  In this order:
+ *   x = scale q . k_t
+ *   x <- softcap tanh(x / softcap)
+ *   x <- x - slopes[query head] (p - t)
+ * t is visible if t < min(prefix[b], seq_lens[b]), or if
+ * max(doc_start[b][i], p - window + 1, 0) <= t <= p.  The prefix is seen by all
+ * of the call's queries, before and behind their own position, whatever the
+ * window and the document (attention sinks, a prompt attended both ways). */
+typedef struct {
+  double scale;                /* 0: 1/sqrt(128); else finite, 0 < scale <= 1e30 */
+  double softcap;              /* 0: none; else 1e-30..1e30 */
+  int32_t window;              /* 0: none; else a query sees its own position and the window - 1 before it */
+  int32_t reserved;            /* not read */
+  const float* d_slopes;       /* fp32 [n_q_heads], finite; NULL: no bias */
+  const int32_t* d_prefix;     /* int32 [batch]; NULL: 0 (values clamped to 0..seq_lens) */
+  const int32_t* d_doc_start;  /* int32 [batch][n_q]; NULL: 0 */
+} bgtq_score;
+
+/* Attention of the last n_q tokens of each sequence (1: a decode step; more:
+ * tokens drafted or verified together, causal among themselves) over the
+ * 8-bit cache, which holds their own rows too.
+ *   d_q, d_out   fp16 or bf16 [layer_count][batch][n_q][n_q_heads][128]
+ *   d_seq_lens   int32 [batch], 0..capacity, the new tokens counted
+ *   n_q          1..max_q_tokens
+ *   score        host memory, read before the call returns; NULL: the defaults
+ * Scores, softmax statistics and sums are fp32; the softmax weights are
+ * rounded to fp16 before they meet the (exact) codes.  A query that sees
+ * nothing gives 0 (so do queries before position 0, where n_q >
+ * seq_lens[b]).  A length out of range sets BGTQ_DEVERR_SEQ_LEN and counts
+ * as 0; a page id outside the pool sets BGTQ_DEVERR_PAGE and page 0 is read.
+ * Results do not depend on the batch's other sequences beyond the order of
+ * floating-point sums, and are the same each time.  Uses the workspace: two
+ * such calls on one state must not overlap on the GPU (captured graphs that
+ * hold one included).  Two launches.  ASYNC. */
+int bgtq_byte_decode_attn(bgtq_state* st, int32_t layer, int32_t layer_count, const void* d_q,
+                          const int32_t* d_seq_lens, int32_t batch, int32_t n_q, const bgtq_score* score, void* d_out,
+                          void* stream);
 
 /* Synchronises "stream", reads the device error flag into *h_flags
  * (BGTQ_DEVERR_* bits) and clears it.  SYNC. */

@@ -62,6 +62,34 @@ class _Config(ctypes.Structure):
     ]
 
 
+class _ByteConfig(ctypes.Structure):
+    _fields_ = [
+        ("n_layers", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("n_q_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("max_batch", ctypes.c_int32),
+        ("code", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("max_q_tokens", ctypes.c_int32),
+        ("page_pool_tiles", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("capacity_tokens", ctypes.c_int64),
+    ]
+
+
+class _Score(ctypes.Structure):
+    _fields_ = [
+        ("scale", ctypes.c_double),
+        ("softcap", ctypes.c_double),
+        ("window", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("d_slopes", ctypes.c_void_p),
+        ("d_prefix", ctypes.c_void_p),
+        ("d_doc_start", ctypes.c_void_p),
+    ]
+
+
 @dataclass
 class Config:
     """Mirror of bgtq_config."""
@@ -84,6 +112,39 @@ class Config:
         c = _Config()
         for f in fields(self):
             setattr(c, f.name, getattr(self, f.name))
+        return c
+
+    @property
+    def group_size(self):
+        return self.n_q_heads // self.n_kv_heads
+
+
+CODES = {"e4m3": 0, "int8": 1}
+ROWS = {"fp16": 0, "bf16": 1}
+
+
+@dataclass
+class ByteConfig:
+    """Mirror of bgtq_byte_config, with its enums by name."""
+    n_layers: int
+    n_kv_heads: int
+    n_q_heads: int
+    max_batch: int
+    capacity_tokens: int
+    code: str = "e4m3"         # "e4m3" or "int8"
+    rows: str = "fp16"         # type of rows, queries and outputs: "fp16" or "bf16"
+    max_q_tokens: int = 1
+    page_pool_tiles: int = 0   # > 0: paged cache (pages per layer and KV head)
+    head_dim: int = HEAD_DIM
+
+    def to_c(self):
+        c = _ByteConfig()
+        if self.code not in CODES or self.rows not in ROWS:
+            raise BgtqError(-1, f"code {self.code!r}, rows {self.rows!r}: expected one of {list(CODES)}, {list(ROWS)}")
+        for f in ("n_layers", "n_kv_heads", "n_q_heads", "head_dim", "max_batch", "max_q_tokens", "page_pool_tiles",
+                  "capacity_tokens"):
+            setattr(c, f, getattr(self, f))
+        c.code, c.dtype, c.reserved = CODES[self.code], ROWS[self.rows], 0
         return c
 
     @property
@@ -124,6 +185,12 @@ _SIGS = {
     "bgtq_set_split_tokens": (ctypes.c_int, [_VP, _I32]),
     "bgtq_set_decode_path": (ctypes.c_int, [_VP, _I32]),
     "bgtq_get_decode_path": (ctypes.c_int, [_VP, _VP, _VP]),
+    "bgtq_byte_required_bytes": (ctypes.c_int, [ctypes.POINTER(_ByteConfig), ctypes.POINTER(ctypes.c_size_t),
+                                                ctypes.POINTER(ctypes.c_size_t)]),
+    "bgtq_byte_create": (ctypes.c_int, [ctypes.POINTER(_ByteConfig), _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP,
+                                        ctypes.POINTER(_VP)]),
+    "bgtq_byte_append": (ctypes.c_int, [_VP, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _I32, _VP]),
+    "bgtq_byte_decode_attn": (ctypes.c_int, [_VP, _I32, _I32, _VP, _VP, _I32, _I32, _VP, _VP, _VP]),
     "bgtq_get_device_error": (ctypes.c_int, [_VP, _VP, _VP]),
     "bgtq_error_string": (ctypes.c_char_p, [_I32]),
 }
@@ -347,6 +414,34 @@ def bgtq_get_decode_path(state):
     out, ctas = ctypes.c_int32(0), ctypes.c_int32(0)
     _check(lib().bgtq_get_decode_path(state, ctypes.byref(out), ctypes.byref(ctas)))
     return out.value, ctas.value
+
+
+def bgtq_byte_required_bytes(cfg):
+    c = cfg.to_c()
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().bgtq_byte_required_bytes(ctypes.byref(c), ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
+
+def bgtq_byte_create(cfg, d_cache, cache_bytes, d_workspace, workspace_bytes, stream=None):
+    c = cfg.to_c()
+    out = _VP()
+    _check(lib().bgtq_byte_create(ctypes.byref(c), _ptr(d_cache), cache_bytes, _ptr(d_workspace), workspace_bytes,
+                                  _stream(stream), ctypes.byref(out)))
+    return out.value
+
+
+def bgtq_byte_append(state, layer, layer_count, d_k, d_v, d_start, d_count, batch, n, stream=None):
+    _check(lib().bgtq_byte_append(state, layer, layer_count, _ptr(d_k), _ptr(d_v), _ptr(d_start), _ptr(d_count),
+                                  batch, n, _stream(stream)))
+
+
+def bgtq_byte_decode_attn(state, layer, layer_count, d_q, d_seq_lens, batch, n_q, d_out, scale=0.0, softcap=0.0,
+                          window=0, d_slopes=None, d_prefix=None, d_doc_start=None, stream=None):
+    """The score's fields by keyword (bgtq_score)."""
+    score = _Score(scale, softcap, window, 0, _ptr(d_slopes), _ptr(d_prefix), _ptr(d_doc_start))
+    _check(lib().bgtq_byte_decode_attn(state, layer, layer_count, _ptr(d_q), _ptr(d_seq_lens), batch, n_q,
+                                       ctypes.addressof(score), _ptr(d_out), _stream(stream)))
 
 
 def bgtq_get_device_error(state, stream=None):
@@ -585,6 +680,135 @@ class PackedKVCache:
     def decode_wave_ctas(self):
         """CTAs one wave of the decode kernel holds (the automatic split plan's budget)."""
         return bgtq_get_decode_path(self.state)[1]
+
+    def device_error(self):
+        return bgtq_get_device_error(self.state)
+
+
+class ByteKVCache:
+    """One 8-bit cache (bgtq_byte_create) over torch-owned device buffers: e4m3
+    or int8 codes with one power-of-two scale per 64 positions and KV head.
+
+    A decode step, per layer ``l``::
+
+        kv = ByteKVCache(ByteConfig(n_layers=36, n_kv_heads=2, n_q_heads=16, max_batch=1,
+                                    capacity_tokens=131072, code="int8", rows="bf16"), "cuda")
+        kv.append(l, k, v, start, count)              # prefill, then each step's rows
+        kv.decode_attn(l, q, seq_lens, out)           # q [1, batch, n_q, n_q_heads, 128]
+    """
+
+    def __init__(self, cfg, device="cuda"):
+        import torch
+        self.cfg = cfg
+        self.device = torch.device(device)
+        self.cache_bytes, self.workspace_bytes = bgtq_byte_required_bytes(cfg)
+        self.cache = torch.zeros(self.cache_bytes, dtype=torch.uint8, device=self.device)
+        self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+        self.state = bgtq_byte_create(cfg, self.cache, self.cache_bytes, self.workspace, self.workspace_bytes)
+        self.offsets = bgtq_cache_offsets(self.state)
+
+    def close(self):
+        if getattr(self, "state", None):
+            bgtq_destroy(self.state)
+            self.state = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def row_dtype(self):
+        import torch
+        return torch.bfloat16 if self.cfg.rows == "bf16" else torch.float16
+
+    # -- views of the cache arrays (no copies) --
+    def _slots(self):
+        """Leading dims of the arrays: (L, B, Hkv, T) contiguous, (L, Hkv, pages) paged."""
+        c = self.cfg
+        if c.page_pool_tiles > 0:
+            return (c.n_layers, c.n_kv_heads, c.page_pool_tiles)
+        return (c.n_layers, c.max_batch, c.n_kv_heads, (c.capacity_tokens + TILE - 1) // TILE)
+
+    def _codes(self, at):
+        import torch
+        s = self._slots()
+        n = int(np.prod(s)) * TILE * HEAD_DIM
+        dt = torch.float8_e4m3fn if self.cfg.code == "e4m3" else torch.int8
+        return self.cache[at:at + n].view(dt).view(*s, TILE, HEAD_DIM)
+
+    def _scales(self, at):
+        import torch
+        s = self._slots()
+        return self.cache[at:at + 4 * int(np.prod(s))].view(torch.float32).view(*s)
+
+    def k_codes(self):
+        """K codes [L, B, Hkv, T, 64, 128] (paged: [L, Hkv, pages, 64, 128]), float8_e4m3fn or int8."""
+        return self._codes(self.offsets[0])
+
+    def k_scales(self):
+        """K scales fp32 [L, B, Hkv, T] (paged: [L, Hkv, pages])."""
+        return self._scales(self.offsets[1])
+
+    def v_codes(self):
+        return self._codes(self.offsets[2])
+
+    def v_scales(self):
+        return self._scales(self.offsets[3])
+
+    # -- calls (tensors checked as PackedKVCache checks its own) --
+    def append(self, layer, k, v, start, count, layer_count=1):
+        """k, v [layer_count, batch, n, Hkv, 128] of the cache's row type; start, count int32 [batch]."""
+        import torch
+        _expect(k, "k", (layer_count, None, None, self.cfg.n_kv_heads, HEAD_DIM), self.row_dtype, self.device)
+        _expect(v, "v", tuple(k.shape), self.row_dtype, self.device)
+        _expect(start, "start", (k.shape[1],), torch.int32, self.device)
+        _expect(count, "count", (k.shape[1],), torch.int32, self.device)
+        bgtq_byte_append(self.state, layer, layer_count, k, v, start, count, k.shape[1], k.shape[2])
+
+    def decode_attn(self, layer, q, seq_lens, out, layer_count=1, scale=None, softcap=0.0, slopes=None, window=0,
+                    prefix=None, doc_start=None):
+        """Attention of the last n_q tokens of each sequence.
+
+        q, out: [layer_count, batch, n_q, Hq, 128] of the cache's row type; seq_lens
+        int32 [batch], the new tokens counted.  scale: of q . k (None:
+        1/sqrt(128)).  softcap c: scores become c tanh(x / c).  slopes fp32
+        [Hq]: slope * distance is taken off.  window: positions a query sees,
+        its own included.  prefix int32 [batch]: positions below it are seen by
+        every query.  doc_start int32 [batch, n_q]: the first position of each
+        query's document.
+        """
+        import torch
+        dt = self.row_dtype
+        _expect(q, "q", (layer_count, None, None, self.cfg.n_q_heads, HEAD_DIM), dt, self.device)
+        _expect(out, "out", tuple(q.shape), dt, self.device)
+        batch, n_q = q.shape[1], q.shape[2]
+        _expect(seq_lens, "seq_lens", (batch,), torch.int32, self.device)
+        if slopes is not None:
+            _expect(slopes, "slopes", (self.cfg.n_q_heads,), torch.float32, self.device)
+        if prefix is not None:
+            _expect(prefix, "prefix", (batch,), torch.int32, self.device)
+        if doc_start is not None:
+            _expect(doc_start, "doc_start", (batch, n_q), torch.int32, self.device)
+        if scale is not None and not scale > 0:
+            raise BgtqError(ERR_INVALID_ARG, f"scale: {scale}, expected a positive number")
+        bgtq_byte_decode_attn(self.state, layer, layer_count, q, seq_lens, batch, n_q, out, scale or 0.0, softcap,
+                              window, slopes, prefix, doc_start)
+
+    def set_block_table(self, table):
+        """Paged cache: int32 [max_batch, ceil(capacity / 64)] page ids on the
+        device (kept referenced here; read at kernel time)."""
+        import torch
+        c = self.cfg
+        if c.page_pool_tiles > 0 and table is not None:
+            _expect(table, "table", (c.max_batch, (c.capacity_tokens + TILE - 1) // TILE), torch.int32, self.device)
+        bgtq_set_block_table(self.state, table)
+        self._block_table = table
+
+    def test_drop_tile_copies(self, tile):
+        """Test hook: the split pass skips the copies of block `tile` (-1: off)."""
+        _check(lib().bgtq_test_drop_tile_copies(self.state, tile))
 
     def device_error(self):
         return bgtq_get_device_error(self.state)

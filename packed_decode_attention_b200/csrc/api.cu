@@ -14,31 +14,13 @@
 #include "../../include/bgtq.h"
 #include "device_tables.h"
 #include "host_tables.h"
+#include "state.h"
 
+using bgtq::aligned16;
+using bgtq::as_stream;
+using bgtq::check_device;
 using bgtq::kD;
-
-struct bgtq_state {
-  bgtq_config cfg;
-  bgtq::Shape shape;
-  bgtq::Workspace ws;
-  bgtq::CacheDev cache;
-  size_t cache_off[4];
-  size_t cache_bytes, ws_bytes;
-  int split_tokens = 0;  // 0 = automatic
-  int ctas_per_sm = 0;   // resident decode CTAs per SM (looked up on first use)
-  int fused_clusters = -1;  // co-resident clusters of the fused decode (looked up on first use; 0: not usable)
-  int fused_cluster_size = 8;
-  int decode_mode = 0;      // 1: the fused decode where the GPU can run it; 0: rotation + split + combine
-  int num_sms = 148;
-  int device = -1;       // the CUDA device current at bgtq_create: its buffers live there
-  bool ready = false;
-  bool have_energy = false;
-  std::vector<int8_t> widths;                    // [L][Hkv][64]
-  std::vector<bgtq::GroupLayout> layouts;        // [L][Hkv]
-  std::vector<float> krot;                       // [L][Hkv][4][128*128] per group, row-major d x d
-  std::vector<float> vrot;                       // [L][Hkv][128*128]
-  std::vector<uint64_t> energy_q, energy_k;      // [L][Hkv][64][2]
-};
+using bgtq::layer_range_ok;
 
 namespace {
 
@@ -48,15 +30,6 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // Allocation set, and for a paged cache a block table given.
 bool cache_ready(const bgtq_state* st) { return st->ready && (st->cache.n_pages == 0 || st->cache.block_table); }
-
-// A call that launches or copies runs on the device the state was created
-// on: its cache, workspace and tables live there, and a launch on another
-// device would read them through the wrong context.
-int check_device(const bgtq_state* st) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return BGTQ_ERR_CUDA;
-  return dev == st->device ? BGTQ_OK : BGTQ_ERR_INVALID_ARG;
-}
 
 constexpr int kMaxLayers = 65535;
 
@@ -141,15 +114,6 @@ Layout plan(const bgtq_config* c) {
   p.ws_total = align_up(p.comb_count + qrows * sizeof(uint32_t));
   return p;
 }
-
-// layers [layer, layer + layer_count) of the config (no overflow for any int32 inputs)
-bool layer_range_ok(const bgtq_config& c, int32_t layer, int32_t layer_count) {
-  return layer >= 0 && layer < c.n_layers && layer_count >= 1 && layer_count <= c.n_layers - layer;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 uint32_t half_bits(float x) {
   const __half h = __float2half_rn(x);
@@ -462,6 +426,7 @@ void bgtq_destroy(bgtq_state* st) { delete st; }
 
 int bgtq_allocate(bgtq_state* st, const void* d_calib_q, int32_t nq, const void* d_calib_k, int32_t nk, void* stream) {
   if (!st || !d_calib_q || !d_calib_k) return BGTQ_ERR_NULL;
+  if (st->byte) return BGTQ_ERR_INVALID_ARG;
   if (nq < 1 || nk < 1) return BGTQ_ERR_INVALID_ARG;
   const int dv = check_device(st);
   if (dv != BGTQ_OK) return dv;
@@ -508,6 +473,7 @@ int bgtq_allocate(bgtq_state* st, const void* d_calib_q, int32_t nq, const void*
 
 int bgtq_set_allocation(bgtq_state* st, const int8_t* h_widths, void* stream) {
   if (!st || !h_widths) return BGTQ_ERR_NULL;
+  if (st->byte) return BGTQ_ERR_INVALID_ARG;
   const int dv = check_device(st);
   if (dv != BGTQ_OK) return dv;
   const bgtq_config& c = st->cfg;
@@ -1010,6 +976,7 @@ int bgtq_test_drop_tile_copies(bgtq_state* st, int32_t tile) {
 
 int bgtq_set_split_tokens(bgtq_state* st, int32_t tokens) {
   if (!st) return BGTQ_ERR_NULL;
+  if (st->byte) return BGTQ_ERR_INVALID_ARG;
   if (tokens < 0 || tokens % bgtq::kSplitGranule != 0) return BGTQ_ERR_INVALID_ARG;
   if (tokens > 0 && (st->cfg.capacity_tokens + tokens - 1) / tokens > max_splits_of(&st->cfg)) return BGTQ_ERR_INVALID_ARG;
   st->split_tokens = tokens;
@@ -1018,6 +985,7 @@ int bgtq_set_split_tokens(bgtq_state* st, int32_t tokens) {
 
 int bgtq_set_decode_path(bgtq_state* st, int32_t fused) {
   if (!st) return BGTQ_ERR_NULL;
+  if (st->byte) return BGTQ_ERR_INVALID_ARG;
   if (fused != 0 && fused != 1) return BGTQ_ERR_INVALID_ARG;
   st->decode_mode = fused;
   return BGTQ_OK;
@@ -1025,6 +993,7 @@ int bgtq_set_decode_path(bgtq_state* st, int32_t fused) {
 
 int bgtq_get_decode_path(bgtq_state* st, int32_t* h_fused, int32_t* h_ctas) {
   if (!st || !h_fused || !h_ctas) return BGTQ_ERR_NULL;
+  if (st->byte) return BGTQ_ERR_INVALID_ARG;
   if (const int dv = check_device(st)) return dv;
   const bool f = use_fused(st);
   *h_fused = f ? 1 : 0;

@@ -1,0 +1,211 @@
+// Append to the 8-bit cache: rows of K and V are quantised to e4m3 or int8
+// codes with one power-of-two scale per (layer, page, KV head, K or V) block
+// of 64 positions.
+//
+//   a = max |x| over the block's new rows, e = the least integer with
+//   a <= Qmax 2^e (Qmax 448 or 127), code = round(x 2^-e) to nearest even.
+//
+// A power-of-two scale makes x 2^-e exact, so a code is rounded once, and a
+// block whose scale grows with a later row (a call that starts inside it)
+// rescales its old codes by a power of two: exact in e4m3 down to its
+// subnormals, one more rounding in int8.  The price is at most one bit of
+// int8's range against a scale of a / 127.
+#include <cuda_bf16.h>
+
+#include "byte_cache.h"
+#include "common.cuh"
+
+namespace bgtq {
+
+namespace {
+
+constexpr int kAppThreads = 256;
+
+// The least e >= kByteMinExp with a <= Qmax 2^e, from a's bits (finite, >= 0).
+__device__ __forceinline__ int block_exp(float a, int code) {
+  // a = (1 + f 2^-23) 2^(x - 127); subnormals fall under the least exponent
+  const uint32_t u = __float_as_uint(a);
+  const int x = static_cast<int>(u >> 23) - 126;
+  const uint32_t f = u & 0x7FFFFFu;
+  const int e = code == 0 ? x - 9 + (f > 0x600000u) : x - 7 + (f > 0x7E0000u);
+  return e < kByteMinExp ? kByteMinExp : e;
+}
+
+// 2^e, e in [-126, 127].
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// Two values (already scaled) to two codes; NaN to 0, values past the range to the largest code.
+__device__ __forceinline__ uint32_t encode2(float x, float y, int code) {
+  if (code == 0) {
+    x = x == x ? x : 0.f;
+    y = y == y ? y : 0.f;
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+    return r;
+  }
+  const int a = max(-127, min(127, __float2int_rn(x))), b = max(-127, min(127, __float2int_rn(y)));
+  return (a & 255) | ((b & 255) << 8);
+}
+
+// Two codes as values.
+__device__ __forceinline__ float2 decode2(uint32_t w, int code) {
+  if (code == 0) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
+  }
+  return make_float2(static_cast<float>(static_cast<int8_t>(w & 255)), static_cast<float>(static_cast<int8_t>(w >> 8 & 255)));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 row2(uint32_t w) {
+  if constexpr (BF16) return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
+  return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+
+// A CTA per (layer, sequence, block, KV head, K or V), heads next to one
+// another in the grid so that neighbouring CTAs read a row's neighbouring
+// heads.  Thread (r, c) of the 16 x 16 holds dimensions 8 c .. 8 c + 7 of
+// rows r, r + 16, r + 32, r + 48: 64 bytes in flight a thread, and a row's
+// 256 bytes are one warp half's load.  Bound by HBM: 2 bytes read and 1
+// written an element; the conversion is about a third of that time's issue
+// slots.
+template <bool BF16>
+__global__ __launch_bounds__(kAppThreads) void byte_append_kernel(ByteShape sh, ByteCacheDev cache,
+                                                                  const int32_t* __restrict__ table, uint32_t* err,
+                                                                  int layer0, const uint16_t* __restrict__ k,
+                                                                  const uint16_t* __restrict__ v,
+                                                                  const int32_t* __restrict__ start_v,
+                                                                  const int32_t* __restrict__ count_v, int batch, int n,
+                                                                  int blocks_per_seq) {
+  const int tid = threadIdx.x;
+  int64_t id = blockIdx.x;
+  const int h = id % sh.n_kv_heads;
+  id /= sh.n_kv_heads;
+  const int kind = id & 1;
+  id >>= 1;
+  const int tb = id % blocks_per_seq;
+  id /= blocks_per_seq;
+  const int b = id % batch, li = id / batch;
+  const int layer = layer0 + li;
+  const int start = start_v[b], count = count_v[b];
+  if (start < 0 || count < 0 || count > n) {
+    if (tid == 0) atomicOr(err, kErrArg);
+    return;
+  }
+  int64_t end = static_cast<int64_t>(start) + count;
+  if (end > sh.capacity) {
+    if (tid == 0) atomicOr(err, kErrCapacity);
+    end = sh.capacity;
+  }
+  const int64_t t = start / kByteBlock + tb;
+  if (t * kByteBlock >= end) return;
+  int64_t slot;
+  if (sh.n_pages == 0) {
+    slot = ((static_cast<int64_t>(layer) * sh.max_batch + b) * sh.n_kv_heads + h) * sh.ntiles + t;
+  } else {
+    const int32_t page = __ldcg(table + static_cast<int64_t>(b) * sh.ntiles + t);
+    if (page < 0 || page >= sh.n_pages) {
+      if (tid == 0) atomicOr(err, kErrPage);
+      return;
+    }
+    slot = (static_cast<int64_t>(layer) * sh.n_kv_heads + h) * sh.n_pages + page;
+  }
+  uint8_t* codes = cache.codes[kind] + slot * kByteTileBytes;
+  float* scale = cache.scales[kind] + slot;
+  const int r = tid >> 4, c = tid & 15;
+  const int64_t lo = max(static_cast<int64_t>(start), t * kByteBlock) - t * kByteBlock;  // written positions [lo, hi)
+  const int64_t hi = min(end, (t + 1) * kByteBlock) - t * kByteBlock;
+  const float old_scale = lo > 0 ? __ldcg(scale) : 0.f;
+
+  // the new rows' elements, and their largest finite magnitude
+  const uint16_t* x = (kind == 0 ? k : v) +
+                      ((static_cast<int64_t>(li) * batch + b) * n + (t * kByteBlock - start)) * sh.n_kv_heads * 128 +
+                      h * 128 + 8 * c;
+  uint4 w[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int p = r + 16 * s;
+    w[s] = p >= lo && p < hi ? __ldcs(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(p) * sh.n_kv_heads * 128))
+                             : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float amax = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const uint32_t u[4] = {w[s].x, w[s].y, w[s].z, w[s].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = row2<BF16>(u[j]);
+      const float a = fabsf(f.x), d = fabsf(f.y);
+      if (a < CUDART_INF_F) amax = fmaxf(amax, a); else bad = true;
+      if (d < CUDART_INF_F) amax = fmaxf(amax, d); else bad = true;
+    }
+  }
+  __shared__ uint32_t red[kAppThreads / 32];
+  const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+  if ((tid & 31) == 0) red[tid >> 5] = wm;
+  if (bad) atomicOr(err, kErrNonFinite);
+  __syncthreads();
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kAppThreads / 32; ++i) m = max(m, red[i]);
+  int e = block_exp(__uint_as_float(m), sh.code);
+  int grow = 0;  // e - e_old where the block's other codes are to be rescaled
+  if (lo > 0) {
+    // a block nothing was written to has no power of two in its place: as the least scale
+    int e_old = static_cast<int>(__float_as_uint(old_scale) >> 23) - 127;
+    if (!(old_scale > 0.f) || e_old < kByteMinExp || e_old > 127) e_old = kByteMinExp;
+    if (e > e_old) grow = e - e_old;
+    else e = e_old;
+  }
+  const float inv = pow2(-e);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int p = r + 16 * s;
+    uint2* at = reinterpret_cast<uint2*>(codes + p * 128 + 8 * c);
+    uint32_t out[4];
+    if (p >= lo && p < hi) {
+      const uint32_t u[4] = {w[s].x, w[s].y, w[s].z, w[s].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = row2<BF16>(u[j]);
+        out[j] = encode2(f.x * inv, f.y * inv, sh.code);
+      }
+    } else if (grow > 0) {
+      const uint2 was = *at;
+      const float down = grow > 126 ? 0.f : pow2(-grow);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = decode2((j < 2 ? was.x : was.y) >> (16 * (j & 1)) & 0xFFFFu, sh.code);
+        out[j] = encode2(f.x * down, f.y * down, sh.code);
+      }
+    } else {
+      continue;
+    }
+    *at = make_uint2(out[0] | out[1] << 16, out[2] | out[3] << 16);
+  }
+  if (tid == 0) *scale = pow2(e);
+}
+
+}  // namespace
+
+cudaError_t launch_byte_append(const ByteShape& s, const ByteCacheDev& c, const int32_t* block_table, uint32_t* err,
+                               int layer0, int layer_count, const void* k, const void* v, const int32_t* start,
+                               const int32_t* count, int batch, int n, cudaStream_t stream) {
+  // n rows touch at most this many blocks, wherever they start
+  const int per_seq = (n - 1) / kByteBlock + (n > 1 ? 2 : 1);
+  const int64_t ctas = static_cast<int64_t>(layer_count) * batch * per_seq * 2 * s.n_kv_heads;
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const uint16_t* kp = static_cast<const uint16_t*>(k);
+  const uint16_t* vp = static_cast<const uint16_t*>(v);
+  if (s.bf16)
+    byte_append_kernel<true><<<static_cast<unsigned>(ctas), kAppThreads, 0, stream>>>(
+        s, c, block_table, err, layer0, kp, vp, start, count, batch, n, per_seq);
+  else
+    byte_append_kernel<false><<<static_cast<unsigned>(ctas), kAppThreads, 0, stream>>>(
+        s, c, block_table, err, layer0, kp, vp, start, count, batch, n, per_seq);
+  return cudaGetLastError();
+}
+
+}  // namespace bgtq
