@@ -27,6 +27,14 @@
  *                          capped, distance-biased, windowed, prefix- and
  *                          document-masked scores
  *
+ * For both caches:
+ *
+ *   bgtq_copy_pages / _fork_sequences / _resize_sequences / _compact_pages
+ *                          pages of a paged cache shared, copied, freed,
+ *                          reserved and moved together
+ *   bgtq_rope_axes         rotary positions over one or several axes for the
+ *                          query and key rows of a step
+ *
  * Conventions
  *  - Every function returns 0 (BGTQ_OK) or a negative BGTQ_ERR_* code and
  *    never throws or aborts.  Argument checks happen before any launch; a
@@ -102,8 +110,9 @@ enum {
   BGTQ_DEVERR_NONFINITE = 8,   /* allocate: a calibration value is Inf or NaN; byte_append: a row's element is
                                   (stored as the largest code, NaN as 0) */
   BGTQ_DEVERR_TIMEOUT = 16,    /* decode: a wait for a tile copy gave up (bounded spin) */
-  BGTQ_DEVERR_PAGE = 32        /* paged cache: a block-table entry outside [0, page_pool_tiles) (encode skips the
+  BGTQ_DEVERR_PAGE = 32,       /* paged cache: a block-table entry outside [0, page_pool_tiles) (encode skips the
                                   tile, decode reads page 0 instead, logit MAE skips the tile) */
+  BGTQ_DEVERR_POOL = 64        /* fork_sequences, resize_sequences: no free page was left for some row */
 };
 
 typedef struct {
@@ -449,7 +458,8 @@ int bgtq_get_decode_path(bgtq_state* st, int32_t* h_fused, int32_t* h_ctas);
  * layouts, paging and call conventions.  No calibration, rotation or
  * allocation comes before it.  A state made by bgtq_byte_create works with
  * bgtq_destroy, bgtq_cache_offsets, bgtq_set_block_table,
- * bgtq_test_drop_tile_copies, bgtq_get_device_error and the calls below; the
+ * bgtq_test_drop_tile_copies, bgtq_get_device_error, the page operations and
+ * the calls below; the
  * packed cache's other calls answer BGTQ_ERR_NOT_READY or
  * BGTQ_ERR_INVALID_ARG for it, and the bgtq_byte_* calls
  * BGTQ_ERR_INVALID_ARG for a packed state.
@@ -549,6 +559,112 @@ typedef struct {
 int bgtq_byte_decode_attn(bgtq_state* st, int32_t layer, int32_t layer_count, const void* d_q,
                           const int32_t* d_seq_lens, int32_t batch, int32_t n_q, const bgtq_score* score, void* d_out,
                           void* stream);
+
+/* ---- Pages of a paged cache, packed or 8-bit ------------------------------
+ *
+ * A page id names the same 64 positions' slots in every layer and KV head.
+ * The caller keeps, in device memory, the block table int32 [batch][ceil(
+ * capacity / 64)], the lengths int32 [batch] (row b holds its table's first
+ * ceil(lens[b] / 64) entries) and reference counts int32 [page_pool_tiles]:
+ * how many rows hold a page, and one more for every other owner (a prompt
+ * kept for later requests); 0: free.  Entries behind a row's last page are
+ * neither read nor written, but for those that a resize frees.  The calls
+ * work on a state of either kind with page_pool_tiles > 0
+ * (BGTQ_ERR_INVALID_ARG otherwise), whether or not a block table is set, and
+ * for the packed cache before or after an allocation.  They take pages from
+ * the lowest free id up, in the order of the rows, so the same inputs give
+ * the same tables.  Pointers are 4-byte aligned; outputs lie apart from the
+ * inputs and one another, except where "may be" says so
+ * (BGTQ_ERR_INVALID_ARG).  1 <= batch <= max_batch.  d_scratch: device memory of
+ * bgtq_page_scratch_bytes bytes whose contents are lost; calls that overlap on
+ * the GPU need one each (captured graphs included).
+ * A length out of 0..capacity sets BGTQ_DEVERR_SEQ_LEN and counts as 0; a page
+ * id in use out of 0..page_pool_tiles - 1 sets BGTQ_DEVERR_PAGE. */
+
+/* Bytes of d_scratch (16 a row and 12 a page of the pool).  SYNC (host only). */
+int bgtq_page_scratch_bytes(const bgtq_state* st, size_t* bytes);
+
+/* Copies page src[i] to page dst[i], i < n, for every layer and KV head
+ * (codes, norms or scales as they are).  A page may be copied to several, but
+ * no page may be in d_dst twice, nor in both lists (i = i aside, which does
+ * nothing): which bytes it then holds is not defined.  A pair with an id
+ * outside the pool is skipped and sets BGTQ_DEVERR_PAGE.  One launch.  ASYNC. */
+int bgtq_copy_pages(bgtq_state* st, const int32_t* d_src, const int32_t* d_dst, int32_t n, void* stream);
+
+/* Row b becomes a fork of row parent[b], -1: empty (freed).  Beam search,
+ * parallel samples of a prompt, rows leaving.  Whole pages are shared; a page
+ * that a row fills partly, which it will write next, ends up with one holder:
+ * of the rows that take it over the first keeps it (unless a row or owner
+ * besides them holds it too), the others get copies.
+ *   d_parent     int32 [batch], -1..batch - 1 (else BGTQ_DEVERR_ARG, taken as -1)
+ *   d_table, d_refs, d_lens            before
+ *   d_table_out, d_refs_out, d_lens_out  after; refs_out may be refs, lens_out
+ *                lens; table_out is another table (copy it back, or point
+ *                bgtq_set_block_table to it)
+ * Where the pool has no page left for a copy: BGTQ_DEVERR_POOL, the row's entry
+ * is -1 and its length that of its whole pages.  Two launches.  ASYNC. */
+int bgtq_fork_sequences(bgtq_state* st, const int32_t* d_parent, const int32_t* d_table, const int32_t* d_refs,
+                        const int32_t* d_lens, int32_t batch, int32_t* d_table_out, int32_t* d_refs_out,
+                        int32_t* d_lens_out, void* d_scratch, void* stream);
+
+/* Takes row b from lens[b] to new_lens[b] positions.  Shorter (drafted tokens
+ * rejected; 0: freed): the pages behind its last one are given back, their
+ * entries -1.  Longer: it gets pages for all of its positions, and where its
+ * last page is filled partly and shared, a copy of it (by the same rule as a
+ * fork), so that positions lens[b] .. new_lens[b] - 1 may be written.  Pages
+ * given back in the call are handed out in the same call.
+ *   d_table, d_refs   before and after
+ *   d_lens_out        the lengths granted; may be d_lens or d_new_lens
+ * Where the pool runs out: BGTQ_DEVERR_POOL, and lens_out[b] is the length the
+ * row got pages for (lens[b] where no page was left to copy its last one to).
+ * A new length out of range sets BGTQ_DEVERR_SEQ_LEN and changes nothing for
+ * its row.  Two launches.  ASYNC. */
+int bgtq_resize_sequences(bgtq_state* st, int32_t* d_table, int32_t* d_refs, const int32_t* d_lens,
+                          const int32_t* d_new_lens, int32_t batch, int32_t* d_lens_out, void* d_scratch,
+                          void* stream);
+
+/* Moves the live pages (refs > 0) to ids 0 .. n_live - 1: the k-th live page
+ * from n_live on goes to the k-th free one below.
+ *   d_table_out  the rows' entries renamed; may be d_table
+ *   d_refs_out   the counts at the new ids; may be d_refs
+ *   d_map        int32 [page_pool_tiles]: each page's new id, -1 for a free one
+ *                (for owners besides the table's rows)
+ *   d_n_live     int32 [1]
+ * An entry that names a free page becomes -1 and sets BGTQ_DEVERR_PAGE.  Two
+ * launches.  ASYNC. */
+int bgtq_compact_pages(bgtq_state* st, const int32_t* d_table, const int32_t* d_refs, const int32_t* d_lens,
+                       int32_t batch, int32_t* d_table_out, int32_t* d_refs_out, int32_t* d_map, int32_t* d_n_live,
+                       void* d_scratch, void* stream);
+
+/* ---- Rotary positions over several axes ----------------------------------- */
+
+typedef struct {
+  int32_t n_q_heads;         /* >= 0, <= 65536 */
+  int32_t n_kv_heads;        /* >= 0, <= 65536; one of both > 0 */
+  int32_t head_dim;          /* must be 128 */
+  int32_t pairing;           /* as bgtq_config's rope_pairing */
+  int32_t dtype;             /* BGTQ_DTYPE_* */
+  int32_t n_axes;            /* 1..64 (time, height, width: 3; 1: plain RoPE) */
+  uint8_t axis[64];          /* block j turns with axis[j] < n_axes */
+  double base;               /* finite, > 1 */
+} bgtq_rope_config;
+
+/* Turns query and key rows before they meet a cache: block j of token n by
+ * the angle pos[axis[j]][n] base^(-2j/128), (a, b) -> (a cos - b sin, a sin +
+ * b cos).  Angles in fp64, sines and products in fp32, one rounding.
+ *   cfg            host memory, read before the call returns
+ *   d_q, d_q_out   fp16 or bf16, n_q_heads x 128 in a row a token, the tokens
+ *                  `stride` elements apart (a multiple of 8, up to 2^30): a
+ *                  slice of a projection's output will do
+ *   d_k, d_k_out   likewise with n_kv_heads; not read where that is 0
+ *   d_pos          int32 [n_axes][tokens], any values
+ * An output may be its input (same pointer and stride); else outputs lie apart
+ * from the inputs and one another (slices of the same rows do).  Rows are
+ * 16-byte aligned, d_pos 4.  0 <= tokens <= 2^30.  Works on the current
+ * device, whose memory the pointers must be.  One launch.  ASYNC. */
+int bgtq_rope_axes(const bgtq_rope_config* cfg, const void* d_q, int32_t q_stride, const void* d_k, int32_t k_stride,
+                   const int32_t* d_pos, int32_t tokens, void* d_q_out, int32_t q_out_stride, void* d_k_out,
+                   int32_t k_out_stride, void* stream);
 
 /* Synchronises "stream", reads the device error flag into *h_flags
  * (BGTQ_DEVERR_* bits) and clears it.  SYNC. */

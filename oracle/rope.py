@@ -41,3 +41,18 @@ def apply_rope(x_rows, positions, base, pairing=0):
         out[:, a] = x[:, a] * c - x[:, b] * s
         out[:, b] = x[:, a] * s + x[:, b] * c
     return out
+
+
+def apply_rope_axes(x_rows, positions, axis, base, pairing=0):
+    """Rows x [n, D] turned by positions [axes][n]: block j by positions[axis[j]] * theta_j (time, height and width
+    of images and video; every block on axis 0 gives ``apply_rope``)."""
+    x = np.asarray(x_rows, dtype=np.float64)
+    pos = np.asarray(positions, dtype=np.float64)
+    theta = inv_freq(x.shape[1], base)
+    out = np.empty_like(x)
+    for j, (a, b) in enumerate(block_dims(x.shape[1], pairing)):
+        ang = pos[axis[j]] * theta[j]
+        c, s = np.cos(ang), np.sin(ang)
+        out[:, a] = x[:, a] * c - x[:, b] * s
+        out[:, b] = x[:, a] * s + x[:, b] * c
+    return out

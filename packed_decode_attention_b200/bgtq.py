@@ -35,6 +35,7 @@ DEVERR_ARG = 4
 DEVERR_NONFINITE = 8
 DEVERR_TIMEOUT = 16
 DEVERR_PAGE = 32
+DEVERR_POOL = 64
 
 
 class BgtqError(RuntimeError):
@@ -87,6 +88,19 @@ class _Score(ctypes.Structure):
         ("d_slopes", ctypes.c_void_p),
         ("d_prefix", ctypes.c_void_p),
         ("d_doc_start", ctypes.c_void_p),
+    ]
+
+
+class _RopeConfig(ctypes.Structure):
+    _fields_ = [
+        ("n_q_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("pairing", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("axis", ctypes.c_uint8 * N_BLOCKS),
+        ("base", ctypes.c_double),
     ]
 
 
@@ -191,6 +205,13 @@ _SIGS = {
                                         ctypes.POINTER(_VP)]),
     "bgtq_byte_append": (ctypes.c_int, [_VP, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _I32, _VP]),
     "bgtq_byte_decode_attn": (ctypes.c_int, [_VP, _I32, _I32, _VP, _VP, _I32, _I32, _VP, _VP, _VP]),
+    "bgtq_copy_pages": (ctypes.c_int, [_VP, _VP, _VP, _I32, _VP]),
+    "bgtq_page_scratch_bytes": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_size_t)]),
+    "bgtq_fork_sequences": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP]),
+    "bgtq_resize_sequences": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP]),
+    "bgtq_compact_pages": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "bgtq_rope_axes": (ctypes.c_int, [ctypes.POINTER(_RopeConfig), _VP, _I32, _VP, _I32, _VP, _I32, _VP, _I32, _VP, _I32,
+                                      _VP]),
     "bgtq_get_device_error": (ctypes.c_int, [_VP, _VP, _VP]),
     "bgtq_error_string": (ctypes.c_char_p, [_I32]),
 }
@@ -444,6 +465,46 @@ def bgtq_byte_decode_attn(state, layer, layer_count, d_q, d_seq_lens, batch, n_q
                                        ctypes.addressof(score), _ptr(d_out), _stream(stream)))
 
 
+def bgtq_page_scratch_bytes(state):
+    n = ctypes.c_size_t()
+    _check(lib().bgtq_page_scratch_bytes(state, ctypes.byref(n)))
+    return n.value
+
+
+def bgtq_copy_pages(state, d_src, d_dst, n, stream=None):
+    _check(lib().bgtq_copy_pages(state, _ptr(d_src), _ptr(d_dst), n, _stream(stream)))
+
+
+def bgtq_fork_sequences(state, d_parent, d_table, d_refs, d_lens, batch, d_table_out, d_refs_out, d_lens_out,
+                        d_scratch, stream=None):
+    _check(lib().bgtq_fork_sequences(state, _ptr(d_parent), _ptr(d_table), _ptr(d_refs), _ptr(d_lens), batch,
+                                     _ptr(d_table_out), _ptr(d_refs_out), _ptr(d_lens_out), _ptr(d_scratch),
+                                     _stream(stream)))
+
+
+def bgtq_resize_sequences(state, d_table, d_refs, d_lens, d_new_lens, batch, d_lens_out, d_scratch, stream=None):
+    _check(lib().bgtq_resize_sequences(state, _ptr(d_table), _ptr(d_refs), _ptr(d_lens), _ptr(d_new_lens), batch,
+                                       _ptr(d_lens_out), _ptr(d_scratch), _stream(stream)))
+
+
+def bgtq_compact_pages(state, d_table, d_refs, d_lens, batch, d_table_out, d_refs_out, d_map, d_n_live, d_scratch,
+                       stream=None):
+    _check(lib().bgtq_compact_pages(state, _ptr(d_table), _ptr(d_refs), _ptr(d_lens), batch, _ptr(d_table_out),
+                                    _ptr(d_refs_out), _ptr(d_map), _ptr(d_n_live), _ptr(d_scratch),
+                                    _stream(stream)))
+
+
+def bgtq_rope_axes(n_q_heads, n_kv_heads, pairing, dtype, axis, base, d_q, q_stride, d_k, k_stride, d_pos, n_axes,
+                   tokens, d_q_out, q_out_stride, d_k_out, k_out_stride, head_dim=HEAD_DIM, stream=None):
+    """The config's fields first (bgtq_rope_config); axis: 64 integers."""
+    if len(axis) != N_BLOCKS or any(int(x) != x or not 0 <= x < 256 for x in axis):
+        raise BgtqError(ERR_INVALID_ARG, f"axis: expected {N_BLOCKS} axis numbers")
+    c = _RopeConfig(n_q_heads, n_kv_heads, head_dim, pairing, dtype, n_axes, (ctypes.c_uint8 * N_BLOCKS)(*map(int, axis)),
+                    float(base))
+    _check(lib().bgtq_rope_axes(ctypes.byref(c), _ptr(d_q), q_stride, _ptr(d_k), k_stride, _ptr(d_pos), tokens,
+                                _ptr(d_q_out), q_out_stride, _ptr(d_k_out), k_out_stride, _stream(stream)))
+
+
 def bgtq_get_device_error(state, stream=None):
     f = ctypes.c_int32()
     _check(lib().bgtq_get_device_error(state, _stream(stream), ctypes.byref(f)))
@@ -454,7 +515,118 @@ def bgtq_error_string(status):
     return lib().bgtq_error_string(status).decode()
 
 
-class PackedKVCache:
+def rope_axes(q, k, pos, axis, base, q_out=None, k_out=None, pairing=0):
+    """Turns query and key rows by rotary positions over several axes (bgtq_rope_axes).
+
+    q [tokens, Hq, 128], k [tokens, Hkv, 128] (either may be None): fp16 or bf16,
+    heads contiguous, tokens any multiple of 8 elements apart (a slice of a
+    projection's output).  pos int32 [axes, tokens]; axis: the axis of each of
+    the 64 blocks.  q_out, k_out: None for new tensors, or q, k themselves.
+    Returns (q_out, k_out).
+    """
+    import torch
+    if q is None and k is None:
+        raise BgtqError(ERR_INVALID_ARG, "q, k: one of them is needed")
+    one = k if q is None else q
+    if not isinstance(one, torch.Tensor) or one.dtype not in (torch.float16, torch.bfloat16) or one.dim() != 3:
+        raise BgtqError(ERR_INVALID_ARG, "q, k: fp16 or bf16 tensors [tokens, heads, 128] are expected")
+    tokens, dev = one.shape[0], one.device
+
+    def rows(t, name, heads):
+        if t is None:
+            return 0, 0
+        _expect(t[:1].contiguous() if isinstance(t, torch.Tensor) and t.dim() == 3 else t, name,
+                (min(1, tokens), heads, HEAD_DIM), one.dtype, dev)
+        if (t.shape[0] != tokens or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != HEAD_DIM) or
+                t.stride(0) >= 1 << 31 or tokens >= 1 << 31):
+            raise BgtqError(ERR_INVALID_ARG, f"{name}: {tuple(t.shape)}, strides {t.stride()}: expected {tokens} tokens "
+                                             "of contiguous heads")
+        # a single token has no next one: its stride says nothing
+        return t.shape[1], t.stride(0) if tokens > 1 else t.shape[1] * HEAD_DIM
+
+    hq, sq = rows(q, "q", None)
+    hkv, sk = rows(k, "k", None)
+    if q is not None and q_out is None:
+        q_out = torch.empty((tokens, hq, HEAD_DIM), dtype=q.dtype, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty((tokens, hkv, HEAD_DIM), dtype=k.dtype, device=dev)
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise BgtqError(ERR_INVALID_ARG, "q_out, k_out: given without q, k")
+    sqo, sko = rows(q_out, "q_out", hq)[1], rows(k_out, "k_out", hkv)[1]
+    _expect(pos, "pos", (None, tokens), torch.int32, dev)
+    if dev.type == "cuda" and torch.cuda.current_device() != dev.index:
+        raise BgtqError(ERR_INVALID_ARG, f"q, k: on {dev}, which is not the current device")
+    if tokens > 0:
+        bgtq_rope_axes(hq, hkv, pairing, 1 if one.dtype == torch.bfloat16 else 0, axis, base, q, sq, k, sk, pos,
+                       pos.shape[0], tokens, q_out, sqo, k_out, sko)
+    return q_out, k_out
+
+
+class _Pages:
+    """The page operations of a paged cache (include/bgtq.h: rows' block table
+    int32 [batch, ceil(capacity / 64)], refs int32 [pages], lens int32 [batch],
+    all on the device)."""
+
+    page_scratch = None
+
+    def _make_page_scratch(self):
+        import torch
+        if self.cfg.page_pool_tiles > 0:
+            self.page_scratch = torch.empty(bgtq_page_scratch_bytes(self.state), dtype=torch.uint8, device=self.device)
+
+    def _page_args(self, batch, tables=(), refs=(), per_row=()):
+        import torch
+        width = (self.cfg.capacity_tokens + TILE - 1) // TILE
+        for t, name in tables:
+            _expect(t, name, (batch, width), torch.int32, self.device)
+        for t, name in refs:
+            _expect(t, name, (self.cfg.page_pool_tiles,), torch.int32, self.device)
+        for t, name in per_row:
+            _expect(t, name, (batch,), torch.int32, self.device)
+
+    def copy_pages(self, src, dst):
+        """Page src[i] to dst[i] (int32 [n]); no page twice in dst or in both lists."""
+        import torch
+        _expect(src, "src", (None,), torch.int32, self.device)
+        _expect(dst, "dst", tuple(src.shape), torch.int32, self.device)
+        if src.shape[0] > 0:
+            bgtq_copy_pages(self.state, src, dst, src.shape[0])
+
+    def fork_sequences(self, parent, table, refs, lens, table_out, refs_out, lens_out):
+        """Row b becomes a fork of row parent[b] (-1: empty): whole pages shared, partly filled ones copied for
+        every holder but one.  refs_out may be refs, lens_out lens; table_out is another table."""
+        import torch
+        _expect(parent, "parent", (None,), torch.int32, self.device)
+        batch = parent.shape[0]
+        self._page_args(batch, ((table, "table"), (table_out, "table_out")), ((refs, "refs"), (refs_out, "refs_out")),
+                        ((lens, "lens"), (lens_out, "lens_out")))
+        bgtq_fork_sequences(self.state, parent, table, refs, lens, batch, table_out, refs_out, lens_out,
+                            self.page_scratch)
+
+    def resize_sequences(self, table, refs, lens, new_lens, lens_out):
+        """Row b from lens[b] to new_lens[b] positions: pages given back (0: all) or taken, a shared last page copied
+        before it is written.  table and refs change in place; lens_out: the lengths granted (may be lens or
+        new_lens)."""
+        import torch
+        _expect(lens, "lens", (None,), torch.int32, self.device)
+        batch = lens.shape[0]
+        self._page_args(batch, ((table, "table"),), ((refs, "refs"),), ((new_lens, "new_lens"), (lens_out, "lens_out")))
+        bgtq_resize_sequences(self.state, table, refs, lens, new_lens, batch, lens_out, self.page_scratch)
+
+    def compact_pages(self, table, refs, lens, table_out, refs_out, page_map, n_live):
+        """Live pages (refs > 0) move to ids 0 .. n_live - 1.  page_map int32 [pages]: new ids, -1 for free ones;
+        n_live int32 [1].  table_out may be table, refs_out refs."""
+        import torch
+        _expect(lens, "lens", (None,), torch.int32, self.device)
+        _expect(n_live, "n_live", (1,), torch.int32, self.device)
+        batch = lens.shape[0]
+        self._page_args(batch, ((table, "table"), (table_out, "table_out")),
+                        ((refs, "refs"), (refs_out, "refs_out"), (page_map, "page_map")))
+        bgtq_compact_pages(self.state, table, refs, lens, batch, table_out, refs_out, page_map, n_live,
+                           self.page_scratch)
+
+
+class PackedKVCache(_Pages):
     """One library state over torch-owned device buffers."""
 
     def __init__(self, cfg, device="cuda"):
@@ -466,6 +638,7 @@ class PackedKVCache:
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         self.state = bgtq_create(cfg, self.cache, self.cache_bytes, self.workspace, self.workspace_bytes)
         self.offsets = bgtq_cache_offsets(self.state)
+        self._make_page_scratch()
 
     def close(self):
         if getattr(self, "state", None):
@@ -685,7 +858,7 @@ class PackedKVCache:
         return bgtq_get_device_error(self.state)
 
 
-class ByteKVCache:
+class ByteKVCache(_Pages):
     """One 8-bit cache (bgtq_byte_create) over torch-owned device buffers: e4m3
     or int8 codes with one power-of-two scale per 64 positions and KV head.
 
@@ -706,6 +879,7 @@ class ByteKVCache:
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         self.state = bgtq_byte_create(cfg, self.cache, self.cache_bytes, self.workspace, self.workspace_bytes)
         self.offsets = bgtq_cache_offsets(self.state)
+        self._make_page_scratch()
 
     def close(self):
         if getattr(self, "state", None):

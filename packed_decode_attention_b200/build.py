@@ -7,7 +7,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libbgtq.so")
 SOURCES = ["csrc/encode.cu", "csrc/decode.cu", "csrc/diag.cu", "csrc/api.cu", "csrc/host_tables.cpp",
-           "csrc/byte_append.cu", "csrc/byte_decode.cu", "csrc/api_byte.cu"]
+           "csrc/byte_append.cu", "csrc/byte_decode.cu", "csrc/api_byte.cu", "csrc/pages.cu", "csrc/api_pages.cu",
+           "csrc/rope.cu", "csrc/api_rope.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
@@ -19,7 +20,7 @@ NVCC_FLAGS = [
 def sources():
     return [os.path.join(PKG, s) for s in SOURCES] + [
         os.path.join(PKG, "csrc", h) for h in ("device_tables.h", "host_tables.h", "common.cuh",
-                                                      "byte_cache.h", "state.h")] + [
+                                                      "byte_cache.h", "pages.h", "rope.h", "state.h")] + [
         os.path.join(ROOT, "include", "bgtq.h")]
 
 

@@ -1,6 +1,5 @@
-// Launch parameters of the 8-bit cache (byte_append.cu, byte_decode.cu), the
-// page operations (pages.cu) and the rotary positions over several axes
-// (rope.cu), shared by the kernels and the C ABI (api_byte.cu).
+// Launch parameters of the 8-bit cache (byte_append.cu, byte_decode.cu),
+// shared by the kernels and the C ABI (api_byte.cu).
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -1,0 +1,471 @@
+// Pages of a paged cache, packed or 8-bit: copying, forking, resizing and
+// compacting.
+//
+// A page id names the same page of every layer and KV head; refs[p] counts
+// who holds page p (rows of the block table and other owners), 0: free.
+//
+//   plan kernels  one cluster of 8 CTAs turns parents, lengths and counts
+//                 into a new table, new counts and a list of page pairs
+//   copy kernel   moves the pairs' bytes, for every layer and head
+//
+// The plans touch a few words a table entry and are bound by latency: each
+// step between two cluster barriers is a few trips to L2.  The copy is bound
+// by HBM: every byte of a copied page is read once and written once.
+#include "common.cuh"
+#include "pages.h"
+
+namespace bgtq {
+
+namespace {
+
+constexpr int kPlanCtas = 8;          // the largest portable cluster
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanAll = kPlanCtas * kPlanThreads;
+constexpr int kPlanChunk = 128;       // table entries a warp takes at once
+constexpr uint32_t kErrPool = 64;
+
+// All CTAs of the plan's cluster, with their global writes.
+__device__ __forceinline__ void plan_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ int pages_for(int len) { return len / kTile + (len % kTile != 0); }
+
+// Exclusive sum of x over the CTA's threads, and the total.
+template <typename T>
+__device__ __forceinline__ T plan_scan(T x, T* red, T& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();
+  if (lane == 31) red[warp] = incl;
+  __syncthreads();
+  T before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWarps; ++w) {
+    if (w < warp) before += red[w];
+    total += red[w];
+  }
+  return before + incl - x;
+}
+
+// Calls f(p, k) for each page p of [lo, hi) with pred(p), k its rank among
+// them plus base, in ascending order; returns base plus their number.
+template <typename P, typename F>
+__device__ __forceinline__ int plan_select(int lo, int hi, int base, int* red, P pred, F f) {
+  for (int64_t c = lo; c < hi; c += 4 * kPlanThreads) {
+    const int64_t p = c + 4 * threadIdx.x;
+    bool in[4];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      in[i] = p + i < hi && pred(static_cast<int>(p + i));
+      n += in[i];
+    }
+    int total;
+    int k = base + plan_scan(n, red, total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (in[i]) f(static_cast<int>(p + i), k++);
+    base += total;
+  }
+  return base;
+}
+
+__device__ __forceinline__ int plan_count(int lo, int hi, int* red, const int32_t* refs, bool live) {
+  int n = 0;
+  for (int64_t p = lo + threadIdx.x; p < hi; p += kPlanThreads) {
+    const int r = __ldcg(refs + p);
+    n += live ? r > 0 : r == 0;
+  }
+  int total;
+  plan_scan(n, red, total);
+  return total;
+}
+
+__device__ __forceinline__ int checked_len(const PagePlanArgs& a, int len) {
+  if (len >= 0 && len <= a.capacity) return len;
+  atomicOr(a.err, kErrSeqLen);
+  return 0;
+}
+
+__device__ __forceinline__ bool page_ok(const PagePlanArgs& a, int id) {
+  if (id >= 0 && id < a.n_pages) return true;
+  atomicOr(a.err, kErrPage);
+  return false;
+}
+
+// fork:   row b becomes row parent[b]; the last page, where the row fills it
+//         partly, is shared by nobody afterwards
+// resize: rows give back pages or get new ones; a partly filled page that a
+//         growing row shares is copied for it
+// Both end the same way: rows that need pages get the free ones in ascending
+// order of the pages, in the order of the rows.
+template <int OP>
+__global__ __launch_bounds__(kPlanThreads, 1) void plan_kernel(const __grid_constant__ PagePlanArgs a) {
+  __shared__ int red[kPlanWarps];
+  __shared__ int64_t wide[kPlanWarps];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int rank = blockIdx.x, gid = rank * kPlanThreads + tid, gwarp = gid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // the rows' new lengths, and the partly filled page each would write
+  if (a.refs_out != a.refs)
+    for (int p = gid; p < a.n_pages; p += kPlanAll) a.refs_out[p] = __ldg(a.refs + p);
+  for (int b = gid; b < a.batch; b += kPlanAll) {
+    int row = b, len, part;
+    if constexpr (OP == kPageFork) {
+      row = __ldg(a.parent + b);
+      if (row < -1 || row >= a.batch) {
+        atomicOr(a.err, kErrArg);
+        row = -1;
+      }
+      len = row < 0 ? 0 : checked_len(a, a.lens[row]);
+      part = len;
+    } else {
+      part = checked_len(a, a.lens[b]);
+      len = __ldg(a.new_lens + b);
+      if (len < 0 || len > a.capacity) {
+        atomicOr(a.err, kErrSeqLen);
+        len = part;
+      }
+      if (len <= part) part = 0;  // nothing will be written behind it
+    }
+    int page = -1;
+    if (part % kTile != 0) {
+      page = a.table[row * a.ntiles + part / kTile];
+      if (!page_ok(a, page)) page = -1;
+    }
+    a.ws.page[b] = page;
+    a.ws.len[b] = len;
+  }
+  plan_sync();
+
+  // who holds what now
+  const int64_t chunks = (a.ntiles + kPlanChunk - 1) / kPlanChunk;
+  for (int64_t it = gwarp; it < a.batch * chunks; it += kPlanAll / 32) {
+    const int b = static_cast<int>(it / chunks);
+    const int64_t t0 = (it - b * chunks) * kPlanChunk;
+    const int have = a.lens[b] >= 0 && a.lens[b] <= a.capacity ? pages_for(a.lens[b]) : 0;
+    const int want = pages_for(__ldcg(a.ws.len + b));
+    int row = b;
+    if constexpr (OP == kPageFork) {
+      row = __ldg(a.parent + b);
+      if (row < -1 || row >= a.batch) row = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kPlanChunk / 32; ++i) {
+      const int64_t t = t0 + 32 * i + lane;
+      if constexpr (OP == kPageFork) {
+        if (t < want) {
+          const int id = __ldg(a.table + row * a.ntiles + t);
+          a.table_out[b * a.ntiles + t] = id;
+          if (page_ok(a, id) && row != b) atomicAdd(a.refs_out + id, 1);
+        }
+        if (t < have && row != b) {
+          const int id = __ldg(a.table + b * a.ntiles + t);
+          if (page_ok(a, id)) atomicSub(a.refs_out + id, 1);
+        }
+      } else if (t >= want && t < have) {
+        const int id = a.table[b * a.ntiles + t];
+        a.table_out[b * a.ntiles + t] = -1;
+        if (page_ok(a, id)) atomicSub(a.refs_out + id, 1);
+      }
+    }
+  }
+  plan_sync();
+
+  // a shared partly filled page stays with its first row, unless somebody
+  // else holds it too; the other rows take a page for a copy
+  for (int b = gwarp; b < a.batch; b += kPlanAll / 32) {
+    const int page = __ldcg(a.ws.page + b);
+    int take = 0;
+    if (page >= 0) {
+      int users = 0, before = 0;
+      for (int o = lane; o < a.batch; o += 32) {
+        const bool same = __ldcg(a.ws.page + o) == page;
+        users += same;
+        before += same && o < b;
+      }
+      users = __reduce_add_sync(0xffffffffu, users);
+      before = __reduce_add_sync(0xffffffffu, before);
+      take = before > 0 || __ldcg(a.refs_out + page) > users;
+    }
+    if constexpr (OP == kPageResize) {
+      const int len = __ldcg(a.ws.len + b);
+      const int have = a.lens[b] >= 0 && a.lens[b] <= a.capacity ? pages_for(a.lens[b]) : 0;
+      take |= max(0, pages_for(len) - have) << 1;  // bit 0: the copy; above: new pages
+    }
+    if (lane == 0) a.ws.need[b] = take;
+  }
+  const int per = (a.n_pages + kPlanCtas - 1) / kPlanCtas;
+  const int lo = min(a.n_pages, rank * per), hi = min(a.n_pages, lo + per);
+  {
+    const int n = plan_count(lo, hi, red, a.refs_out, false);
+    if (tid == 0) a.ws.head[8 + rank] = n;
+  }
+  plan_sync();
+
+  int first = 0, n_free = 0;
+#pragma unroll
+  for (int r = 0; r < kPlanCtas; ++r) {
+    const int n = __ldcg(a.ws.head + 8 + r);
+    first += r < rank ? n : 0;
+    n_free += n;
+  }
+  plan_select(
+      lo, hi, first, red, [&](int p) { return __ldcg(a.refs_out + p) == 0; },
+      [&](int p, int k) { a.ws.list[k] = p; });
+  if (rank == 0) {
+    int64_t off = 0;
+    for (int c = 0; c < a.batch; c += kPlanThreads) {
+      const int b = c + tid;
+      const int need = b < a.batch ? __ldcg(a.ws.need + b) : 0;
+      int64_t total;
+      const int64_t at = off + plan_scan(static_cast<int64_t>((need & 1) + (need >> 1)), wide, total);
+      if (b < a.batch) a.ws.off[b] = static_cast<int>(min(at, static_cast<int64_t>(n_free)));
+      off += total;
+    }
+    if (tid == 0) a.ws.head[0] = 0;
+  }
+  plan_sync();
+
+  for (int b = gwarp; b < a.batch; b += kPlanAll / 32) {
+    const int need = __ldcg(a.ws.need + b), off = __ldcg(a.ws.off + b), len = __ldcg(a.ws.len + b);
+    const int take = need & 1, grow = need >> 1;
+    int got = len;
+    if constexpr (OP == kPageFork) {
+      if (take) {
+        const int page = __ldcg(a.ws.page + b), t = len / kTile;
+        const int to = off < n_free ? __ldcg(a.ws.list + off) : -1;
+        if (to < 0) got = t * kTile;
+        if (lane == 0) {
+          a.table_out[b * a.ntiles + t] = to;
+          atomicSub(a.refs_out + page, 1);
+          if (to >= 0) {
+            a.refs_out[to] = 1;
+            const int k = atomicAdd(a.ws.head, 1);
+            a.ws.src[k] = page;
+            a.ws.dst[k] = to;
+          } else {
+            atomicOr(a.err, kErrPool);
+          }
+        }
+      }
+    } else {
+      const int was = a.lens[b] >= 0 && a.lens[b] <= a.capacity ? a.lens[b] : 0;
+      bool full = true;
+      if (take) {
+        const int page = __ldcg(a.ws.page + b);
+        full = off < n_free;
+        if (!full) {
+          got = was;  // the shared page stays as it is
+        } else if (lane == 0) {
+          const int to = __ldcg(a.ws.list + off);
+          a.table_out[b * a.ntiles + was / kTile] = to;
+          atomicSub(a.refs_out + page, 1);
+          a.refs_out[to] = 1;
+          const int k = atomicAdd(a.ws.head, 1);
+          a.ws.src[k] = page;
+          a.ws.dst[k] = to;
+        }
+      }
+      if (grow > 0) {
+        const int have = pages_for(was), can = min(grow, max(0, n_free - off - take));
+        for (int i = lane; i < can; i += 32) {
+          const int to = __ldcg(a.ws.list + off + take + i);
+          a.table_out[b * a.ntiles + have + i] = to;
+          a.refs_out[to] = 1;
+        }
+        if (can < grow) {
+          if (full) got = (have + can) * kTile;
+          full = false;
+        }
+      }
+      if (!full && lane == 0) atomicOr(a.err, kErrPool);
+    }
+    __syncwarp();  // lens_out may be lens
+    if (lane == 0) a.lens_out[b] = got;
+  }
+}
+
+// Live pages move to [0, n_live): the k-th live page at or above n_live takes
+// the k-th hole below it.
+__global__ __launch_bounds__(kPlanThreads, 1) void compact_kernel(const __grid_constant__ PagePlanArgs a) {
+  __shared__ int red[kPlanWarps];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int rank = blockIdx.x, gid = rank * kPlanThreads + tid, gwarp = gid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int per = (a.n_pages + kPlanCtas - 1) / kPlanCtas;
+  const int lo = min(a.n_pages, rank * per), hi = min(a.n_pages, lo + per);
+  {
+    const int n = plan_count(lo, hi, red, a.refs, true);
+    if (tid == 0) a.ws.head[8 + rank] = n;
+  }
+  plan_sync();
+  int first = 0, n_live = 0;
+#pragma unroll
+  for (int r = 0; r < kPlanCtas; ++r) {
+    const int n = __ldcg(a.ws.head + 8 + r);
+    first += r < rank ? n : 0;
+    n_live += n;
+  }
+  // holes below n_live by their ranks; live pages from n_live on by their
+  // ranks among all live ones, counted from the end: both lists then need no
+  // further count.  The j-th live page from the end takes the
+  // (moves - 1 - j)-th hole.
+  const int lo_end = min(hi, n_live), hi_begin = max(lo, n_live);
+  plan_select(
+      lo, lo_end, lo - first, red, [&](int p) { return __ldcg(a.refs + p) <= 0; },
+      [&](int p, int k) { a.ws.dst[k] = p; });
+  {
+    const int mine = lo_end > lo ? plan_count(lo, lo_end, red, a.refs, true) : 0;  // live pages below n_live
+    plan_select(
+        hi_begin, hi, first + mine, red, [&](int p) { return __ldcg(a.refs + p) > 0; },
+        [&](int p, int k) { a.ws.list[n_live - 1 - k] = p; });
+    if (tid == 0) a.ws.head[16 + rank] = mine;
+  }
+  plan_sync();
+  int moves = n_live;
+#pragma unroll
+  for (int r = 0; r < kPlanCtas; ++r) moves -= __ldcg(a.ws.head + 16 + r);
+  if (gid == 0) {
+    a.ws.head[0] = moves;
+    a.n_live[0] = n_live;
+  }
+  // where each page goes, and its count there; a count is read before the
+  // barrier and written behind it, so that refs_out may be refs
+  for (int p = gid; p < a.n_pages; p += kPlanAll) a.map[p] = __ldcg(a.refs + p) > 0 && p < n_live ? p : -1;
+  for (int k = gid; k < moves; k += kPlanAll) {
+    const int src = __ldcg(a.ws.list + moves - 1 - k);
+    a.ws.src[k] = src;
+  }
+  plan_sync();
+  for (int k = gid; k < moves; k += kPlanAll) {
+    const int src = __ldcg(a.ws.src + k), dst = __ldcg(a.ws.dst + k);
+    a.map[src] = dst;
+    a.refs_out[dst] = __ldcg(a.refs + src);
+    if (a.refs_out == a.refs) a.refs_out[src] = 0;
+  }
+  if (a.refs_out != a.refs)
+    for (int p = gid; p < a.n_pages; p += kPlanAll) {
+      const int r = __ldcg(a.refs + p);
+      if (p >= n_live)
+        a.refs_out[p] = min(r, 0);
+      else if (r > 0)
+        a.refs_out[p] = r;
+    }
+  plan_sync();
+  const int64_t chunks = (a.ntiles + kPlanChunk - 1) / kPlanChunk;
+  for (int64_t it = gwarp; it < a.batch * chunks; it += kPlanAll / 32) {
+    const int b = static_cast<int>(it / chunks);
+    const int64_t t0 = (it - b * chunks) * kPlanChunk;
+    const int len = a.lens[b];
+    const bool ok = len >= 0 && len <= a.capacity;
+    if (!ok && lane == 0 && t0 == 0) atomicOr(a.err, kErrSeqLen);
+    const int held = ok ? pages_for(len) : 0;
+#pragma unroll
+    for (int i = 0; i < kPlanChunk / 32; ++i) {
+      const int64_t t = t0 + 32 * i + lane;
+      if (t >= held) continue;
+      const int id = a.table[b * a.ntiles + t];
+      const int to = page_ok(a, id) ? __ldcg(a.map + id) : -1;
+      if (to < 0 && id >= 0 && id < a.n_pages) atomicOr(a.err, kErrPage);  // a free page in the table
+      a.table_out[b * a.ntiles + t] = to;
+    }
+  }
+}
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyCtas = 4;          // per SM
+
+// An item is one (pair, layer, head): a slot of each array.  Four 16-byte
+// loads in flight a thread, 64 KB an SM.
+__global__ __launch_bounds__(kCopyThreads, kCopyCtas) void page_copy_kernel(const __grid_constant__ PageArrays c,
+                                                                            const int32_t* __restrict__ src_v,
+                                                                            const int32_t* __restrict__ dst_v,
+                                                                            int n_pairs, const int32_t* n_pairs_dev,
+                                                                            uint32_t* err) {
+  if (n_pairs_dev != nullptr) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    n_pairs = min(n_pairs, __ldcg(n_pairs_dev));
+  }
+  const int tid = threadIdx.x;
+  int pieces[4], total = 0;            // 16-byte pieces of a slot, array by array
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    pieces[i] = c.bytes[i] >> 4;
+    total += pieces[i];
+  }
+  const int64_t items = n_pairs * c.lh;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t lh = it / n_pairs;
+    const int pair = static_cast<int>(it - lh * n_pairs);
+    const int src = __ldcg(src_v + pair), dst = __ldcg(dst_v + pair);
+    if (src < 0 || src >= c.n_pages || dst < 0 || dst >= c.n_pages) {
+      if (tid == 0) atomicOr(err, kErrPage);
+      continue;
+    }
+    if (src == dst) continue;
+    const int64_t from = lh * c.n_pages + src, to = lh * c.n_pages + dst;
+    for (int base = 0; base < total; base += 4 * kCopyThreads) {
+      uint4 x[4];
+      uint4* at[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        int p = base + j * kCopyThreads + tid;
+        at[j] = nullptr;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (p >= 0 && p < pieces[i]) {
+            x[j] = __ldcs(reinterpret_cast<const uint4*>(c.base[i] + from * c.bytes[i]) + p);
+            at[j] = reinterpret_cast<uint4*>(c.base[i] + to * c.bytes[i]) + p;
+          }
+          p -= pieces[i];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (at[j] != nullptr) __stcs(at[j], x[j]);
+    }
+    if (tid < 4 && c.bytes[tid] == 4)
+      reinterpret_cast<uint32_t*>(c.base[tid])[to] = __ldcs(reinterpret_cast<const uint32_t*>(c.base[tid]) + from);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_page_copy(const PageArrays& c, const int32_t* src, const int32_t* dst, int n_pairs,
+                             const int32_t* n_pairs_dev, uint32_t* err, int n_sms, cudaStream_t stream) {
+  const int64_t items = n_pairs * c.lh, most = static_cast<int64_t>(n_sms) * kCopyCtas;
+  const unsigned grid = static_cast<unsigned>(items < most ? items : most);
+  if (n_pairs_dev != nullptr)
+    return launch_dependent(page_copy_kernel, dim3(grid), dim3(kCopyThreads), 0, stream, c, src, dst, n_pairs,
+                            n_pairs_dev, err);
+  page_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(c, src, dst, n_pairs, nullptr, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_page_plan(PageOp op, const PagePlanArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPlanCtas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kPlanCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (op == kPageFork) return cudaLaunchKernelEx(&cfg, plan_kernel<kPageFork>, a);
+  if (op == kPageResize) return cudaLaunchKernelEx(&cfg, plan_kernel<kPageResize>, a);
+  return cudaLaunchKernelEx(&cfg, compact_kernel, a);
+}
+
+}  // namespace bgtq

@@ -1,5 +1,5 @@
 // The library's state object, shared by the entry points of the packed cache
-// (api.cu) and those of the 8-bit cache and the pages (api_byte.cu).
+// (api.cu), of the 8-bit cache (api_byte.cu) and of the pages (api_pages.cu).
 #pragma once
 #include <stddef.h>
 
