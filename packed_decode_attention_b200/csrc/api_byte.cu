@@ -77,7 +77,7 @@ typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The map of a codes array: rows of 128 bytes, boxes of a block's 64 rows.
+// The map of a codes array: rows of 128 bytes, boxes of half a block's rows.
 int code_map(CUtensorMap* map, void* base, size_t slots) {
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult found;
@@ -85,7 +85,7 @@ int code_map(CUtensorMap* map, void* base, size_t slots) {
     return BGTQ_ERR_CUDA;
   const cuuint64_t dims[2] = {128, slots * bgtq::kByteBlock};
   const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, bgtq::kByteBlock}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {128, bgtq::kByteBlock / 2}, step[2] = {1, 1};
   return reinterpret_cast<EncodeTiled>(fn)(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, step,
                                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -31,7 +31,7 @@ struct ByteCacheDev {
 };
 
 struct ByteAttnArgs {
-  CUtensorMap map[2];             // K, V codes: rows of 128 bytes, boxes of 64 rows, 128-byte swizzle
+  CUtensorMap map[2];             // K, V codes: rows of 128 bytes, boxes of 32 rows, 128-byte swizzle
   const float* scales[2];
   const int32_t* block_table;
   const void* q;

@@ -19,11 +19,14 @@ namespace bgtq {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kRing = 3;                 // 8 KB buffers a warp: K, V and the next K
+constexpr int kStep = 32;                // positions a warp takes at once: half a block
+constexpr int kStepBytes = kStep * 128;
 constexpr int kByteWaitLimit = 1 << 20;  // polls of up to a microsecond each: about a second
 constexpr float kPShift = 14.f;          // softmax weights are held as 2^14 p (see the weights' comment)
+// A unit (one KV head's rows of one sequence) costs a CTA its queries and a
+// merge besides its steps: about as long as this many steps.  Counted when
+// the work is shared out, so that a CTA gets few short sequences.
+constexpr int kUnitCost = 12;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -44,10 +47,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
   return false;
 }
 
-// One block's 64 x 128 codes into shared memory: 16-byte piece c of position
-// p lands at piece c ^ (p & 7) (the map's 128-byte swizzle).
-__device__ __forceinline__ void copy_block(uint32_t dst, const CUtensorMap* map, int32_t row, uint32_t bar) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "n"(kByteTileBytes) : "memory");
+// 32 x 128 codes into shared memory, 16-byte piece c of position p at piece
+// c ^ (p & 7) (the map's 128-byte swizzle).
+__device__ __forceinline__ void copy_step(uint32_t dst, const CUtensorMap* map, int32_t row, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           dst),
@@ -87,78 +89,136 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
   }
 }
 
-// ---- which blocks a sequence's queries see -----------------------------------
+// ---- which steps a sequence's queries see -----------------------------------
 
-struct SeqBlocks {
+struct SeqSteps {
   int32_t len;    // 0 where the given length is out of range
   int32_t pre;    // prefix positions, min(prefix, len)
-  int32_t n_pre;  // blocks 0 .. n_pre - 1 are seen for the prefix alone
-  int32_t t0;     // then blocks t0, t0 + 1, ...
-  int32_t n;      // blocks in all
+  int32_t n_pre;  // steps 0 .. n_pre - 1 are seen for the prefix alone
+  int32_t t0;     // then steps t0, t0 + 1, ...
+  int32_t n;      // steps in all
   bool bad;
 };
 
 __device__ __forceinline__ int32_t query_lo(const ByteAttnArgs& a, int b, int i, int p) {
-  int32_t lo = a.doc_start ? max(0, __ldcg(a.doc_start + static_cast<int64_t>(b) * a.n_q + i)) : 0;
+  int32_t lo = a.doc_start ? max(0, __ldg(a.doc_start + static_cast<int64_t>(b) * a.n_q + i)) : 0;
   if (a.window > 0) lo = max(lo, p - a.window + 1);
   return lo;
 }
 
-__device__ __forceinline__ SeqBlocks seq_blocks(const ByteAttnArgs& a, int b) {
-  SeqBlocks s;
-  const int32_t len = __ldcg(a.seq_lens + b);
+// Loads through L1: a CTA asks again for the sequences that it works on.
+__device__ __forceinline__ SeqSteps seq_steps(const ByteAttnArgs& a, int b) {
+  SeqSteps s;
+  const int32_t len = __ldg(a.seq_lens + b);
   s.bad = len < 0 || len > a.capacity;
   s.len = s.bad ? 0 : len;
-  s.pre = a.prefix ? min(max(0, __ldcg(a.prefix + b)), s.len) : 0;
+  s.pre = a.prefix ? min(max(0, __ldg(a.prefix + b)), s.len) : 0;
   int32_t lo = INT32_MAX;
   if (a.doc_start == nullptr && a.window <= 0) {
     if (s.len > 0) lo = 0;
   } else {
+#pragma unroll 4
     for (int i = 0; i < a.n_q; ++i) {
       const int p = s.len - a.n_q + i;
-      if (p < 0) continue;
       const int32_t l = query_lo(a, b, i, p);
-      if (l <= p) lo = min(lo, l);
+      if (p >= 0 && l <= p) lo = min(lo, l);
     }
   }
-  const int pre_blocks = (s.pre + kByteBlock - 1) / kByteBlock;
+  const int pre_steps = (s.pre + kStep - 1) / kStep;
   if (lo == INT32_MAX) {
-    s.n_pre = s.n = pre_blocks;
+    s.n_pre = s.n = pre_steps;
     s.t0 = 0;
   } else {
-    s.t0 = lo / kByteBlock;
-    s.n_pre = min(pre_blocks, s.t0);
-    s.n = s.n_pre + (s.len - 1) / kByteBlock - s.t0 + 1;
+    s.t0 = lo / kStep;
+    s.n_pre = min(pre_steps, s.t0);
+    s.n = s.n_pre + (s.len - 1) / kStep - s.t0 + 1;
   }
   return s;
 }
 
-// The work is the blocks of all units (layer, KV head, row block) of all
-// sequences, in the order sequence, unit, block; CTA c of `ctas` takes
-// blocks [c N / ctas, (c + 1) N / ctas) whatever units they belong to, so
+// The work is the steps of all units (layer, KV head, row block) of all
+// sequences, in the order sequence, unit, step; each unit is preceded by
+// `pad` places that stand for its own cost.  CTA c of `ctas` takes the places
+// [c V / ctas, (c + 1) V / ctas) of V, whatever units they belong to, so
 // ragged batches are shared evenly.
-__device__ __forceinline__ int active_ctas(int64_t total, int grid) {
-  const int64_t c = (total + kWarps - 1) / kWarps;  // at least a block for each warp
-  return static_cast<int>(c < grid ? (c < 1 ? 1 : c) : grid);
+struct Sums {
+  int64_t v, r;   // places, steps
+  int32_t k;      // sequences that have any
+};
+
+__device__ __forceinline__ int unit_pad(const ByteAttnArgs& a) { return a.batch > 1 ? kUnitCost : 0; }
+__device__ __forceinline__ int places(int n, int pad) { return n > 0 ? n + pad : 0; }
+
+// Quotients whose operands hardly ever need 64 bits.
+__device__ __forceinline__ int64_t quot(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
 }
 
-// The CTA that attends block g.
-__device__ __forceinline__ int cta_of(int64_t g, int64_t total, int ctas) {
-  return static_cast<int>(((g + 1) * ctas - 1) / total);
+// CTA c has places [begin(c), begin(c + 1)): equal shares, or, with per > 0,
+// each unit's steps in `per` equal shares (one sequence: units alike).
+struct Shares {
+  int64_t each;
+  int32_t rem, ctas, per, n;
+  __device__ int64_t begin(int c) const {
+    if (per > 0) {
+      const int u = c / per;
+      return static_cast<int64_t>(u) * n + static_cast<int>(quot(static_cast<int64_t>(c - u * per) * n, per));
+    }
+    return c * each + min(c, rem);
+  }
+  __device__ int of(int64_t g) const {
+    if (per > 0) {
+      const int u = static_cast<int>(quot(g, n));
+      return u * per + static_cast<int>(quot((g - static_cast<int64_t>(u) * n + 1) * per - 1, n));
+    }
+    const int64_t head = rem * (each + 1);
+    return static_cast<int>(g < head ? quot(g, each + 1) : rem + quot(g - head, each));
+  }
+};
+
+// At most a CTA for each `warps` steps or for each unit, whichever are more:
+// a unit's steps are spread over the warps of a CTA first.
+__device__ __forceinline__ Shares shares(const Sums& s, int units, int grid, int warps) {
+  const int64_t c = max(quot(units * s.r + warps - 1, warps), static_cast<int64_t>(units) * s.k);
+  Shares r;
+  r.ctas = static_cast<int>(min(c, static_cast<int64_t>(grid)));
+  r.each = quot(units * s.v, r.ctas);
+  r.rem = static_cast<int32_t>(units * s.v - r.each * r.ctas);
+  r.per = 0;
+  r.n = static_cast<int32_t>(s.r);
+  if (s.v == s.r && units <= r.ctas) {
+    // one sequence: no CTA has steps of two units where the larger shares
+    // cost less than a second unit
+    const int per = r.ctas / units;
+    if (r.n <= per * (r.each + kUnitCost)) {
+      r.per = per;
+      r.ctas = per * units;
+    }
+  }
+  return r;
 }
 
-// Sum over the NT threads; red: NT / 32 places.
+// Sums over the NT threads; red: NT / 32 places.
 template <int NT>
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* red) {
+__device__ __forceinline__ Sums block_sum(Sums x, Sums* red) {
   const int tid = threadIdx.x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    x.v += __shfl_xor_sync(0xffffffffu, x.v, o);
+    x.r += __shfl_xor_sync(0xffffffffu, x.r, o);
+    x.k += __shfl_xor_sync(0xffffffffu, x.k, o);
+  }
   __syncthreads();
   if ((tid & 31) == 0) red[tid >> 5] = x;
   __syncthreads();
-  int64_t s = 0;
+  Sums s{0, 0, 0};
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) s += red[w];
+  for (int w = 0; w < NT / 32; ++w) {
+    s.v += red[w].v;
+    s.r += red[w].r;
+    s.k += red[w].k;
+  }
   return s;
 }
 
@@ -166,59 +226,96 @@ __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* red) {
 
 struct Cursor {
   int b, u, j;
-  SeqBlocks s;
+  int base;       // the unit's first slot (its pool's, where paged)
+  SeqSteps s;
 };
 
-// Moves k blocks on; the caller knows that they exist.
+struct Unit {
+  int li, h, rb;  // layer of the call, KV head, row block
+};
+
+__device__ __forceinline__ Unit unit_of(const ByteAttnArgs& a, int u) {
+  Unit r{0, u, 0};
+  if (a.row_blocks > 1) {
+    r.h = u / a.row_blocks;
+    r.rb = u - r.h * a.row_blocks;
+  }
+  if (a.layer_count > 1) {
+    r.li = r.h / a.hkv;
+    r.h -= r.li * a.hkv;
+  }
+  return r;
+}
+
+// Slots are fewer than 2^25 (the codes' rows have int32 numbers).
+__device__ __forceinline__ int base_of(const ByteAttnArgs& a, int b, int u) {
+  const Unit x = unit_of(a, u);
+  const int layer = a.layer0 + x.li;
+  return a.n_pages == 0 ? ((layer * a.max_batch + b) * a.hkv + x.h) * static_cast<int>(a.ntiles)
+                        : (layer * a.hkv + x.h) * a.n_pages;
+}
+
+// Moves k steps on; the caller knows that they exist.
 __device__ __forceinline__ void advance(const ByteAttnArgs& a, Cursor& c, int units, int k) {
   c.j += k;
-  while (c.j >= c.s.n) {
+  if (c.j < c.s.n) return;
+  do {
     c.j -= c.s.n;
     if (++c.u == units) {
       c.u = 0;
       do {
         if (++c.b >= a.batch) { c.b = a.batch - 1; c.j = 0; return; }
-        c.s = seq_blocks(a, c.b);
+        c.s = seq_steps(a, c.b);
       } while (c.s.n == 0);
     }
-  }
+  } while (c.j >= c.s.n);
+  c.base = base_of(a, c.b, c.u);
 }
 
-struct Place {
-  int32_t tile;
-  int64_t slot;
-};
+__device__ __forceinline__ int tile_of(const SeqSteps& s, int j) { return j < s.n_pre ? j : s.t0 + j - s.n_pre; }
 
-__device__ __forceinline__ Place place_of(const ByteAttnArgs& a, const Cursor& c) {
-  Place r;
-  r.tile = c.j < c.s.n_pre ? c.j : c.s.t0 + c.j - c.s.n_pre;
-  const int lh = c.u / a.row_blocks, li = lh / a.hkv, h = lh - li * a.hkv, layer = a.layer0 + li;
-  if (a.n_pages == 0) {
-    r.slot = ((static_cast<int64_t>(layer) * a.max_batch + c.b) * a.hkv + h) * a.ntiles + r.tile;
-  } else {
-    int32_t page = __ldcg(a.block_table + static_cast<int64_t>(c.b) * a.ntiles + r.tile);
-    if (page < 0 || page >= a.n_pages) {
-      if ((threadIdx.x & 31) == 0) atomicOr(a.err, kErrPage);
-      page = 0;
-    }
-    r.slot = (static_cast<int64_t>(layer) * a.hkv + h) * a.n_pages + page;
+// The slot of a step's block.
+__device__ __forceinline__ int slot_of(const ByteAttnArgs& a, const Cursor& c, int tile) {
+  const int block = tile / (kByteBlock / kStep);
+  if (a.n_pages == 0) return c.base + block;
+  int32_t page = __ldg(a.block_table + static_cast<int64_t>(c.b) * a.ntiles + block);
+  if (page < 0 || page >= a.n_pages) {
+    if ((threadIdx.x & 31) == 0) atomicOr(a.err, kErrPage);
+    page = 0;
   }
-  return r;
+  return c.base + page;
 }
 
-// Shared memory: the warps' rings, then the merge's places.
+// NB blocks of 8 query rows.  One: 12 warps of 168 registers, two pairs of
+// buffers each (a step's K and V); two, with twice the accumulators: 8 warps
+// of 255, three pairs.
 template <int NB>
-struct SplitSmem {
-  static constexpr int kRingBytes = kWarps * kRing * kByteTileBytes;
-  static constexpr int kMergeFloats = NB * (1024 + 16);      // a warp's acc [32][32 lanes] and (m, l) of 8 NB rows
-  static constexpr int kMergeBytes = kWarps / 2 * kMergeFloats * 4;
-  static constexpr int kTotal = 1024 + kRingBytes + kMergeBytes;  // 1024: the swizzle's alignment
+struct Split {
+  static constexpr int kWarps = NB == 1 ? 12 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kRing = NB == 1 ? 2 : 3;         // pairs of buffers
+  static constexpr int kRows = 8 * NB;
+  static constexpr int kQPitch = 136;                   // halves: rows 4 banks apart
+  static constexpr int kUStride = 129;                  // merge: floats from a dimension pair to the next
+  static constexpr int kMergeU = 4;                     // of the 8 pairs of a lane
+  static constexpr int kMergeFloats = kMergeU * kUStride;
+  // shared memory, from a 1024-byte boundary
+  static constexpr int kMergeAt = kWarps * kRing * 2 * kStepBytes;
+  static constexpr int kTotal = 1024 + kMergeAt + kWarps * kMergeFloats * 4;
 };
 
-// NB blocks of 8 query rows against one KV head.  The tensor cores take the
-// codes as the 16-row operand (m16n8k16): positions for q . k, dimensions
-// for p . v, the query rows as the 8 columns, so 8 rows waste nothing and a
-// row block's second 8 rows reuse the widened codes.
+struct Row {
+  float back;     // undoes the query's scaling, times the scores' scale
+  float slope;    // in log2 units
+  int32_t lo, hi; // sees lo .. hi
+  int32_t pre;    // and positions below
+  int32_t tref;   // distances count from here
+  int32_t out;    // its output's place among the sequence's
+};
+
+// The tensor cores take the codes as the 16-row operand (m16n8k16): positions
+// for q . k, dimensions for p . v, the query rows as the 8 columns, so 8 rows
+// waste nothing and a row block's second 8 rows reuse the widened codes.
 //
 // A warp's lane (g, t) = (lane / 4, lane % 4).  K: row g of an M-tile stands
 // for position pi(g) = g / 2 + 4 (g % 2) of its 8, and its K index runs over
@@ -230,202 +327,233 @@ struct SplitSmem {
 //
 // The scores of a lane belong to columns (rows of q) 2 t and 2 t + 1; p is
 // turned into the second product's operand by movmatrix.
-//
-// HBM bound: 16.4 KB a block and KV head.  At the copy rate a block may take
-// about 730 cycles of an SM; its instructions take about 300 (NB = 1).
 template <int CODE, int NB>
-__global__ __launch_bounds__(kThreads, 1) void byte_split_kernel(const __grid_constant__ ByteAttnArgs a) {
+__global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(const __grid_constant__ ByteAttnArgs a) {
+  using C = Split<NB>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads, kRing = C::kRing;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[kWarps * kRing];
-  __shared__ int64_t red[kWarps];
-  __shared__ int64_t found_base;
-  __shared__ int found_b;
+  __shared__ __align__(16) uint16_t qs[C::kRows * C::kQPitch];
+  __shared__ Row row_info[C::kRows];
+  __shared__ float ms[kWarps * C::kRows], ls[kWarps * C::kRows], m_all[C::kRows], l_all[C::kRows];
+  __shared__ Sums red[kWarps];
+  __shared__ int64_t found[4];     // the first sequence, its first place, its first step's number; the end's step
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t ring0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  float* merge = reinterpret_cast<float*>(smem_raw + (ring0 - smem_u32(smem_raw)) + SplitSmem<NB>::kRingBytes);
-  const uint32_t ring = ring0 + warp * kRing * kByteTileBytes;
+  if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(&a.map[tid]) : "memory");
+  const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  float* merge = reinterpret_cast<float*>(smem_raw + (smem0 - smem_u32(smem_raw)) + C::kMergeAt);
+  const uint32_t ring = smem0 + warp * kRing * 2 * kStepBytes;
   const uint32_t bar0 = smem_u32(&bars[warp * kRing]);
-  if (tid < kWarps * kRing) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&bars[tid])) : "memory");
+  if (lane < kRing) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar0 + 8 * lane) : "memory");
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncwarp();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // this CTA's blocks [r0, r1) of the call's
-  const int units = a.layer_count * a.hkv * a.row_blocks;
-  SeqBlocks mine{};
-  int64_t sum = 0;
-  for (int b = tid; b < a.batch; b += kThreads) {
-    const SeqBlocks s = seq_blocks(a, b);
-    if (b == tid) mine = s;
-    if (s.bad && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
-    sum += s.n;
-  }
-  const int64_t total = units * block_sum<kThreads>(sum, red);
-  if (total == 0) return;
-  const int ctas = active_ctas(total, gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const int64_t r0 = blockIdx.x * total / ctas, r1 = (blockIdx.x + 1) * total / ctas;
-  {
-    int64_t before = 0;  // blocks of the sequences before this chunk of 256
+  // this CTA's places [r0, r1), and the steps among them
+  const int units = a.layer_count * a.hkv * a.row_blocks, pad = unit_pad(a);
+  Cursor seg;      // the start of the segment (a unit's steps in this CTA)
+  int mine_total;
+  if (a.batch == 1) {
+    seg.b = 0;
+    seg.s = seq_steps(a, 0);
+    if (seg.s.bad && blockIdx.x == 0 && tid == 0) atomicOr(a.err, kErrSeqLen);
+    if (seg.s.n == 0) return;
+    const Shares sh = shares(Sums{seg.s.n, seg.s.n, 1}, units, gridDim.x, kWarps);
+    if (static_cast<int>(blockIdx.x) >= sh.ctas) return;
+    const int64_t r0 = sh.begin(blockIdx.x);
+    seg.u = static_cast<int>(quot(r0, seg.s.n));
+    seg.j = static_cast<int>(r0 - static_cast<int64_t>(seg.u) * seg.s.n);
+    mine_total = static_cast<int>(sh.begin(blockIdx.x + 1) - r0);
+  } else {
+    int n0 = 0;
+    Sums sum{0, 0, 0};
+    for (int b = tid; b < a.batch; b += kThreads) {
+      const SeqSteps s = seq_steps(a, b);
+      if (b == tid) n0 = s.n;
+      if (s.bad && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
+      sum.v += places(s.n, pad);
+      sum.r += s.n;
+      sum.k += s.n > 0;
+    }
+    sum = block_sum<kThreads>(sum, red);
+    if (sum.r == 0) return;
+    const Shares sh = shares(sum, units, gridDim.x, kWarps);
+    if (static_cast<int>(blockIdx.x) >= sh.ctas) return;
+    const int64_t r0 = sh.begin(blockIdx.x), r1 = sh.begin(blockIdx.x + 1);
+    Sums before{0, 0, 0};  // of the sequences before this chunk
+    if (tid == 0) found[3] = units * sum.r;
     for (int base = 0; base < a.batch; base += kThreads) {
       const int b = base + tid;
-      const int n = b < a.batch ? (base == 0 ? mine.n : seq_blocks(a, b).n) : 0;
-      int64_t incl = n;
+      const int n = b < a.batch ? (base == 0 ? n0 : seq_steps(a, b).n) : 0, np = places(n, pad);
+      // a sequence has fewer than 2^26 places, so 32 of them fit an int32
+      int iv = np, ir = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const int y = __shfl_up_sync(0xffffffffu, iv, o), z = __shfl_up_sync(0xffffffffu, ir, o);
+        if (lane >= o) {
+          iv += y;
+          ir += z;
+        }
       }
       __syncthreads();
-      if (lane == 31) red[warp] = incl;
+      if (lane == 31) red[warp] = Sums{iv, ir, 0};
       __syncthreads();
-      int64_t all = 0;
+      Sums incl{before.v + iv, before.r + ir, 0};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) incl += red[w];
-        all += red[w];
+        if (w < warp) {
+          incl.v += red[w].v;
+          incl.r += red[w].r;
+        }
+        before.v += red[w].v;
+        before.r += red[w].r;
       }
-      const int64_t first = (before + incl - n) * units;
-      if (n > 0 && first <= r0 && r0 < first + static_cast<int64_t>(n) * units) {
-        found_b = b;
-        found_base = first;
+      const int64_t v0 = (incl.v - np) * units, v1 = incl.v * units, s0 = (incl.r - n) * units;
+      if (v0 <= r0 && r0 < v1) {
+        found[0] = b;
+        found[1] = v0;
+        found[2] = s0;
       }
-      before += all;
-      if (before * units > r0) break;
+      if (v0 <= r1 && r1 < v1) {
+        const int64_t off = r1 - v0, u = quot(off, np);
+        found[3] = s0 + u * n + max(static_cast<int64_t>(0), off - u * np - pad);
+      }
+      if (before.v * units > r1) break;
     }
     __syncthreads();
+    seg.b = static_cast<int>(found[0]);
+    seg.s = seq_steps(a, seg.b);
+    const int64_t off = r0 - found[1];
+    const int np = places(seg.s.n, pad);
+    seg.u = static_cast<int>(quot(off, np));
+    seg.j = max(0, static_cast<int>(off - static_cast<int64_t>(seg.u) * np) - pad);
+    mine_total = static_cast<int>(found[3] - found[2] - static_cast<int64_t>(seg.u) * seg.s.n - seg.j);
+    if (mine_total <= 0) return;
   }
-  Cursor seg;  // the start of the segment (a unit's blocks in this CTA's range)
-  seg.b = found_b;
-  seg.s = seq_blocks(a, seg.b);
-  {
-    const int64_t off = r0 - found_base;
-    seg.u = static_cast<int>(off / seg.s.n);
-    seg.j = static_cast<int>(off - static_cast<int64_t>(seg.u) * seg.s.n);
-  }
-  const int mine_total = static_cast<int>(r1 - r0);
+  seg.base = base_of(a, seg.b, seg.u);
 
-  // this warp's blocks: warp, warp + 8, ... of the CTA's; copies run one and
-  // a half blocks ahead (K, V, next K)
+  // this warp's steps: warp, warp + kWarps, ... of the CTA's, kRing of them on
+  // their way
   const int nt = mine_total > warp ? (mine_total - warp + kWarps - 1) / kWarps : 0;
   Cursor cur = seg;
-  float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
-  uint32_t pending = 0;    // bit i: a copy into buffer i is on its way
-  auto issue = [&](int kind, const Place& pl, int buf) {
-    if (pl.tile == a.drop_tile) return;
-    pending |= 1u << buf;
-    if (lane == 0)
-      copy_block(ring + buf * kByteTileBytes, &a.map[kind], static_cast<int32_t>(pl.slot * kByteBlock), bar0 + 8 * buf);
-  };
-  Place ahead{};
-  if (nt > 0) {
-    advance(a, cur, units, warp);
-    const Place p0 = place_of(a, cur);
-    issue(0, p0, 0);
-    issue(1, p0, 1);
-    ks = __ldcg(a.scales[0] + p0.slot);
-    vs = __ldcg(a.scales[1] + p0.slot);
-  }
-  if (nt > 1) {
-    advance(a, cur, units, kWarps);
-    ahead = place_of(a, cur);
-    issue(0, ahead, 2);
-    ks_next = __ldcg(a.scales[0] + ahead.slot);
-    vs_next = __ldcg(a.scales[1] + ahead.slot);
-  }
-  int it = 0;              // the warp's next block
-  int buf = 0;             // its K buffer; its V buffer is the next one
-  uint32_t phases = 0;     // bit i: parity of buffer i's next completion
-  bool dead = false;
-  auto wait = [&](int i) {
-    if (__all_sync(0xffffffffu, bar_wait(bar0 + 8 * i, phases >> i & 1))) {
-      phases ^= 1u << i;
-      pending &= ~(1u << i);
-    } else {
-      dead = true;
+  int issued = 0, ibuf = 0;
+  float ks[kRing], vs[kRing];   // the blocks' scales, the oldest step's first
+  uint32_t pending = 0;         // bit i: copies into pair i are on their way
+  auto issue = [&](float& k, float& v) {
+    if (issued >= nt) return;
+    advance(a, cur, units, issued == 0 ? warp : kWarps);
+    const int tile = tile_of(cur.s, cur.j), slot = slot_of(a, cur, tile);
+    k = __ldg(a.scales[0] + slot);
+    v = __ldg(a.scales[1] + slot);
+    if (tile / (kByteBlock / kStep) != a.drop_tile) {
+      pending |= 1u << ibuf;
+      if (lane == 0) {
+        const uint32_t bar = bar0 + 8 * ibuf, dst = ring + ibuf * 2 * kStepBytes;
+        const int32_t row = slot * kByteBlock + tile % (kByteBlock / kStep) * kStep;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "n"(2 * kStepBytes) : "memory");
+        copy_step(dst, &a.map[0], row, bar);
+        copy_step(dst + kStepBytes, &a.map[1], row, bar);
+      }
     }
+    ++issued;
+    ibuf = ibuf == kRing - 1 ? 0 : ibuf + 1;
   };
-  int f0 = 0;              // blocks of the CTA's range before this segment
+#pragma unroll
+  for (int i = 0; i < kRing; ++i) {
+    ks[i] = vs[i] = 0.f;
+    issue(ks[i], vs[i]);
+  }
+  int it = 0;              // the warp's next step
+  int buf = 0;             // its pair
+  uint32_t phases = 0;     // bit i: parity of pair i's next completion
+  bool dead = false;
+  int f0 = 0;              // steps of the CTA before this segment
   const int pig = (g >> 1) | ((g & 1) << 2);
+  const int rows = a.group * a.n_q;
+
+  // A segment's queries, half a warp a row: asked for before the merge of the
+  // segment before it, everything a row needs at once.
+  struct Asked {
+    uint4 q;
+    float slope;
+    int32_t lo, p, out;
+    bool real;
+  };
+  auto ask = [&](const Cursor& c) {
+    Asked r{make_uint4(0u, 0u, 0u, 0u), 0.f, 1, 0, 0, false};
+    if (warp < C::kRows / 2) {
+      const Unit un = unit_of(a, c.u);
+      const int row = un.rb * C::kRows + 2 * warp + (lane >> 4), i = row / a.group, hg = row - i * a.group;
+      r.real = row < rows;
+      r.p = c.s.len - a.n_q + i;
+      r.out = (i * a.hq + un.h * a.group + hg) * 128;
+      if (r.real) {
+        r.q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                   (static_cast<int64_t>(un.li) * a.batch + c.b) * a.n_q * a.hq * 128 +
+                                                   r.out + 8 * (lane & 15)));
+        if (a.slopes) r.slope = __ldg(a.slopes + un.h * a.group + hg);
+        r.lo = query_lo(a, c.b, i, r.p);
+      }
+    }
+    return r;
+  };
+  Asked asked = ask(seg);
 
   while (f0 < mine_total) {
     const int len_seg = min(seg.s.n - seg.j, mine_total - f0);
-    const int lh = seg.u / a.row_blocks, rb = seg.u - lh * a.row_blocks;
-    const int li = lh / a.hkv, h = lh - li * a.hkv;
-    const int rows = a.group * a.n_q, row0 = rb * 8 * NB;
     const int len = seg.s.len, pre = seg.s.pre;
 
     // q as the products' 8-column operand, scaled by a power of two a row so
     // that its largest element lies in [2^14, 2^15): fp16 and bf16 queries
     // are then both exact in fp16 but for elements under 2^-29 of the
     // largest
-    uint32_t qf[NB][16];
-    float colf[NB][2], slope[NB][2];
-    int lo[NB][2], hi[NB][2], rpre[NB][2], tref[NB][2];
-    int lo_max = 0, hi_min = INT32_MAX;
-    if (it < nt && warp + kWarps * it < f0 + len_seg) {
+    if (warp < C::kRows / 2) {
+      const int rl = 2 * warp + (lane >> 4);
+      const uint4 w = asked.q;
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      float2 x[4];
+      float big = 0.f;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int row = row0 + nb * 8 + g;
-        float x[32];
-        if (row < rows) {
-          const int i = row / a.group, hg = row - i * a.group;
-          const uint16_t* qp = static_cast<const uint16_t*>(a.q) +
-                               (((static_cast<int64_t>(li) * a.batch + seg.b) * a.n_q + i) * a.hq + h * a.group + hg) * 128;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint4 w = *reinterpret_cast<const uint4*>(qp + 16 * (t + 4 * (p >> 1)) + 8 * (p & 1));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = a.bf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]))
-                                      : __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
-              x[8 * p + 2 * e] = f.x;
-              x[8 * p + 2 * e + 1] = f.y;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = 0.f;
-        }
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) m = fmaxf(m, fabsf(x[e]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        // 2^up m in [2^14, 2^15); zero and non-finite rows as they are
-        const int ex = static_cast<int>(__float_as_uint(m) >> 23);
-        const int up = ex == 0 || ex == 255 ? 0 : max(-113, min(113, 141 - ex));
-        const float fac = __int_as_float((up + 127) << 23);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) qf[nb][e] = pack_half2(x[2 * e] * fac, x[2 * e + 1] * fac);
-        const float back = __int_as_float((127 - up) << 23) * a.scale;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          colf[nb][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c));
-          const int r = row0 + nb * 8 + 2 * t + c;
-          if (r < rows) {
-            const int i = r / a.group, hg = r - i * a.group, p = len - a.n_q + i;
-            lo[nb][c] = query_lo(a, seg.b, i, p);
-            hi[nb][c] = p;
-            rpre[nb][c] = pre;
-            lo_max = max(lo_max, lo[nb][c]);
-            hi_min = min(hi_min, p);
-            slope[nb][c] = a.slopes ? __ldg(a.slopes + h * a.group + hg) * kLog2e : 0.f;
-            // distances count from the row's last visible position: its
-            // weights do not change, and the near ones stay exact
-            tref[nb][c] = max(lo[nb][c] <= p ? p : -1, pre - 1);
-          } else {
-            lo[nb][c] = 1;
-            hi[nb][c] = 0;
-            rpre[nb][c] = 0;
-            slope[nb][c] = 0.f;
-            tref[nb][c] = 0;
-          }
-        }
+      for (int e = 0; e < 4; ++e) {
+        x[e] = a.bf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]))
+                      : __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
+        big = fmaxf(big, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
       }
-      lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-      hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      // 2^up m in [2^14, 2^15); zero and non-finite rows as they are
+      const int ex = static_cast<int>(__float_as_uint(big) >> 23);
+      const int up = ex == 0 || ex >= 255 ? 0 : max(-113, min(113, 141 - ex));
+      const float fac = __int_as_float((up + 127) << 23);
+      *reinterpret_cast<uint4*>(qs + rl * C::kQPitch + 8 * (lane & 15)) =
+          make_uint4(pack_half2(x[0].x * fac, x[0].y * fac), pack_half2(x[1].x * fac, x[1].y * fac),
+                     pack_half2(x[2].x * fac, x[2].y * fac), pack_half2(x[3].x * fac, x[3].y * fac));
+      if ((lane & 15) == 0) {
+        Row r{0.f, 0.f, 1, 0, 0, 0, -1};
+        if (asked.real) {
+          r.back = __int_as_float((127 - up) << 23) * a.scale;
+          r.lo = asked.lo;
+          r.hi = asked.p;
+          r.pre = pre;
+          r.slope = asked.slope * kLog2e;
+          // distances count from the row's last visible position: its
+          // weights do not change, and the near ones stay exact
+          r.tref = max(asked.lo <= asked.p ? asked.p : -1, pre - 1);
+          r.out = asked.out;
+        }
+        row_info[rl] = r;
+      }
     }
+    __syncthreads();
+    float colf[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      colf[nb][0] = row_info[nb * 8 + 2 * t].back;
+      colf[nb][1] = row_info[nb * 8 + 2 * t + 1].back;
+    }
+    const bool real = lane < C::kRows && row_info[lane % C::kRows].out >= 0;
+    const int lo_max = __reduce_max_sync(0xffffffffu, real ? row_info[lane].lo : 0);
+    const int hi_min = __reduce_min_sync(0xffffffffu, real ? row_info[lane].hi : INT32_MAX);
 
     float m[NB][2], l[NB][2], acc[NB][8][4];
 #pragma unroll
@@ -438,26 +566,33 @@ __global__ __launch_bounds__(kThreads, 1) void byte_split_kernel(const __grid_co
         for (int e = 0; e < 4; ++e) acc[nb][u][e] = 0.f;
     }
 
+#pragma unroll 1
     for (; it < nt && warp + kWarps * it < f0 + len_seg; ++it) {
-      const int j = seg.j + warp + kWarps * it - f0;
-      const int p0 = kByteBlock * (j < seg.s.n_pre ? j : seg.s.t0 + j - seg.s.n_pre);
-      const int vbuf = buf == kRing - 1 ? 0 : buf + 1;
-      const int nbuf = vbuf == kRing - 1 ? 0 : vbuf + 1;  // the next block's K
-      Place after{};
-      const bool more = it + 2 < nt && !dead;
-      if (more) {
-        advance(a, cur, units, kWarps);
-        after = place_of(a, cur);
-      }
-      if (!dead) wait(buf);
-      float S[NB][4][4];
+      const int p0 = kStep * tile_of(seg.s, seg.j + warp + kWarps * it - f0);
       if (!dead) {
-        const uint32_t kb = ring + buf * kByteTileBytes + pig * 128;
+        if (__all_sync(0xffffffffu, bar_wait(bar0 + 8 * buf, phases >> buf & 1))) {
+          phases ^= 1u << buf;
+          pending &= ~(1u << buf);
+        } else {
+          dead = true;
+        }
+      }
+      if (!dead) {
+        float S[NB][2][4];
+        const uint32_t kb = ring + buf * 2 * kStepBytes + pig * 128, vb = ring + buf * 2 * kStepBytes + kStepBytes;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t piece = ((t + 4 * i) ^ pig) * 16;
+          uint32_t qf[NB][8];
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
+          for (int nb = 0; nb < NB; ++nb) {
+            const uint32_t qa = smem_u32(qs) + ((nb * 8 + g) * C::kQPitch + 64 * i + 16 * t) * 2;
+            const uint4 x = lds128(qa), y = lds128(qa + 16);
+            qf[nb][0] = x.x, qf[nb][1] = x.y, qf[nb][2] = x.z, qf[nb][3] = x.w;
+            qf[nb][4] = y.x, qf[nb][5] = y.y, qf[nb][6] = y.z, qf[nb][7] = y.w;
+          }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
             const uint4 x = lds128(kb + mt * 2048 + piece), y = lds128(kb + mt * 2048 + 1024 + piece);
             const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -470,25 +605,21 @@ __global__ __launch_bounds__(kThreads, 1) void byte_split_kernel(const __grid_co
                 if (i == 0 && w == 0)
                   mma16816_zero(S[nb][mt], a0, a1, a2, a3, qf[nb][0], qf[nb][1]);
                 else
-                  mma16816(S[nb][mt], a0, a1, a2, a3, qf[nb][8 * i + 2 * w], qf[nb][8 * i + 2 * w + 1]);
+                  mma16816(S[nb][mt], a0, a1, a2, a3, qf[nb][2 * w], qf[nb][2 * w + 1]);
               }
             }
           }
         }
-      }
-      __syncwarp();
-      if (it + 1 < nt && !dead) issue(1, ahead, buf);  // the K buffer is free: the next block's V
-      uint32_t pf[NB][4][2];
-      if (!dead) {
-        const bool full = (p0 >= lo_max && p0 + kByteBlock - 1 <= hi_min) || p0 + kByteBlock <= pre;
+        uint32_t pf[NB][2][2];
+        const bool full = (p0 >= lo_max && p0 + kStep - 1 <= hi_min) || p0 + kStep <= pre;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           // scores in log2 units
-          const float f0c = colf[nb][0] * ks, f1c = colf[nb][1] * ks;
+          const float f0c = colf[nb][0] * ks[0], f1c = colf[nb][1] * ks[0];
           if (a.cap > 0.f) {
             const float ic = 1.f / a.cap, oc = a.cap * kLog2e;
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 // tanh u = 1 - 2 / (1 + e^2u); the series' first terms where
@@ -500,30 +631,37 @@ __global__ __launch_bounds__(kThreads, 1) void byte_split_kernel(const __grid_co
               }
           } else {
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
               for (int e = 0; e < 4; ++e) S[nb][mt][e] *= ((e & 1) ? f1c : f0c) * kLog2e;
           }
           if (a.slopes) {
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int c = 0; c < 2; ++c) {
+              const float sl = row_info[nb * 8 + 2 * t + c].slope;
+              const int d0 = p0 + pig - row_info[nb * 8 + 2 * t + c].tref;
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                S[nb][mt][e] += slope[nb][e & 1] * static_cast<float>(p0 + 16 * mt + 8 * (e >> 1) + pig - tref[nb][e & 1]);
+              for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int e = c; e < 4; e += 2) S[nb][mt][e] += sl * static_cast<float>(d0 + 16 * mt + 8 * (e >> 1));
+            }
           }
           if (!full) {
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int c = 0; c < 2; ++c) {
+              const Row r = row_info[nb * 8 + 2 * t + c];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int p = p0 + 16 * mt + 8 * (e >> 1) + pig;
-                const bool see = p < rpre[nb][e & 1] || (p >= lo[nb][e & 1] && p <= hi[nb][e & 1]);
-                if (!see) S[nb][mt][e] = -CUDART_INF_F;
-              }
+              for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int e = c; e < 4; e += 2) {
+                  const int p = p0 + 16 * mt + 8 * (e >> 1) + pig;
+                  if (!(p < r.pre || (p >= r.lo && p <= r.hi))) S[nb][mt][e] = -CUDART_INF_F;
+                }
+            }
           }
           float mx[2] = {m[nb][0], m[nb][1]};
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt)
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e & 1] = fmaxf(mx[e & 1], S[nb][mt][e]);
 #pragma unroll
@@ -550,27 +688,21 @@ __global__ __launch_bounds__(kThreads, 1) void byte_split_kernel(const __grid_co
           const float s0 = mx[0] == -CUDART_INF_F ? 0.f : kPShift - mx[0];
           const float s1 = mx[1] == -CUDART_INF_F ? 0.f : kPShift - mx[1];
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
-            pf[nb][mt][0] = transpose8x8(pack_half2(ex2(S[nb][mt][0] + s0), ex2(S[nb][mt][1] + s1)));
-            pf[nb][mt][1] = transpose8x8(pack_half2(ex2(S[nb][mt][2] + s0), ex2(S[nb][mt][3] + s1)));
-          }
-          // l: the columns' sums of the rounded weights, by ones on the tensor cores
-          float lt[4];
-          mma16816_zero(lt, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pf[nb][0][0], pf[nb][0][1]);
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int mt = 1; mt < 4; ++mt)
-            mma16816(lt, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pf[nb][mt][0], pf[nb][mt][1]);
-          l[nb][0] += lt[0];
-          l[nb][1] += lt[1];
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t w = pack_half2(ex2(S[nb][mt][2 * e] + s0), ex2(S[nb][mt][2 * e + 1] + s1));
+              pf[nb][mt][e] = transpose8x8(w);
+              // the sum is that of the rounded weights; a lane's own positions until the merge
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+              l[nb][0] += f.x;
+              l[nb][1] += f.y;
+            }
         }
-      }
-      if (!dead) wait(vbuf);
-      if (!dead) {
-        const uint32_t vb = ring + vbuf * kByteTileBytes;
-        if (CODE == 0 && p0 + kByteBlock > len) {
+        if (CODE == 0 && p0 + kStep > len) {
           // positions behind the sequence may hold anything, and a NaN code
           // times a zero weight is NaN
-          for (int p = len - p0; p < kByteBlock; ++p)
+          for (int p = len - p0; p < kStep; ++p)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(vb + p * 128 + lane * 4), "r"(0) : "memory");
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
@@ -582,7 +714,7 @@ __global__ __launch_bounds__(kThreads, 1) void byte_split_kernel(const __grid_co
           const uint32_t at0 = vb + t * 128 + ((pig ^ t) * 16) + half * 8;
           const uint32_t at1 = vb + t * 128 + ((pig ^ t ^ 4) * 16) + half * 8;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
+          for (int kk = 0; kk < 2; ++kk) {
             const uint2 x = lds64(at0 + kk * 2048), y = lds64(at1 + kk * 2048 + 512);
             const uint2 z = lds64(at0 + kk * 2048 + 1024), w = lds64(at1 + kk * 2048 + 1536);
 #pragma unroll
@@ -609,107 +741,111 @@ __global__ __launch_bounds__(kThreads, 1) void byte_split_kernel(const __grid_co
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nb][4 * half + u][e] = fmaf(T[nb][u][e], vs, acc[nb][4 * half + u][e]);
+              for (int e = 0; e < 4; ++e) acc[nb][4 * half + u][e] = fmaf(T[nb][u][e], vs[0], acc[nb][4 * half + u][e]);
         }
       }
       __syncwarp();
-      ks = ks_next;
-      vs = vs_next;
-      ahead = after;
-      if (more && !dead) {
-        issue(0, after, vbuf);  // the V buffer is free: K of the block after the next
-        ks_next = __ldcg(a.scales[0] + after.slot);
-        vs_next = __ldcg(a.scales[1] + after.slot);
+#pragma unroll
+      for (int i = 0; i + 1 < kRing; ++i) {
+        ks[i] = ks[i + 1];
+        vs[i] = vs[i + 1];
       }
-      buf = nbuf;
+      if (!dead) issue(ks[kRing - 1], vs[kRing - 1]);  // the pair is free
+      buf = buf == kRing - 1 ? 0 : buf + 1;
     }
 
-    // merge of the 8 warps: a tree through shared memory, in a fixed order
-#pragma unroll 1
-    for (int s = kWarps / 2; s > 0; s >>= 1) {
-      float* at = merge + (warp >= s ? warp - s : warp) * SplitSmem<NB>::kMergeFloats;
-      if (warp >= s && warp < 2 * s) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) at[(nb * 32 + u * 4 + e) * 32 + lane] = acc[nb][u][e];
-          if (g == 0) {
-            float* ml = at + NB * 1024 + nb * 16 + t * 4;
-            ml[0] = m[nb][0];
-            ml[1] = m[nb][1];
-            ml[2] = l[nb][0];
-            ml[3] = l[nb][1];
-          }
-        }
-      }
-      __syncthreads();
-      if (warp < s) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const float* ml = at + NB * 1024 + nb * 16 + t * 4;
-          float ca[2], cb[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float mo = ml[c], mn = fmaxf(m[nb][c], mo);
-            ca[c] = m[nb][c] == mn ? 1.f : ex2(m[nb][c] - mn);
-            cb[c] = mo == mn ? 1.f : ex2(mo - mn);
-            m[nb][c] = mn;
-            l[nb][c] = l[nb][c] * ca[c] + ml[2 + c] * cb[c];
-          }
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              acc[nb][u][e] = acc[nb][u][e] * ca[e & 1] + at[(nb * 32 + u * 4 + e) * 32 + lane] * cb[e & 1];
-        }
-      }
-      __syncthreads();
+    const bool whole = seg.j == 0 && len_seg == seg.s.n;
+    const int place = f0 > 0;
+    uint16_t* const out = static_cast<uint16_t*>(a.out) +
+                          (static_cast<int64_t>(unit_of(a, seg.u).li) * a.batch + seg.b) * a.n_q * a.hq * 128;
+    f0 += len_seg;
+    if (f0 < mine_total) {
+      advance(a, seg, units, len_seg);
+      asked = ask(seg);
     }
-    if (warp == 0) {
-      const bool whole = seg.j == 0 && len_seg == seg.s.n;
+
+    // merge of the warps: their maxima and sums, then the accumulators by
+    // parts through shared memory, a thread summing its elements over the
+    // warps in order
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int rl = nb * 8 + 2 * t + c, row = row0 + rl;
-          if (row >= rows) continue;
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], o);
+        if (g == 0) {
+          ms[warp * C::kRows + nb * 8 + 2 * t + c] = m[nb][c];
+          ls[warp * C::kRows + nb * 8 + 2 * t + c] = l[nb][c];
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float al[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int rl = nb * 8 + 2 * t + c;
+        float mx = -CUDART_INF_F;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ms[w * C::kRows + rl]);
+        al[c] = m[nb][c] == mx ? 1.f : ex2(m[nb][c] - mx);
+        if (warp == 0 && g == 0) {
+          float sum_l = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float mw = ms[w * C::kRows + rl];
+            sum_l += ls[w * C::kRows + rl] * (mw == mx ? 1.f : ex2(mw - mx));
+          }
+          m_all[rl] = mx;
+          l_all[rl] = !whole ? sum_l : sum_l == 0.f ? 0.f : 1.f / sum_l;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nb][u][e] *= al[e & 1];
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int u0 = 0; u0 < 8; u0 += C::kMergeU) {
+        if (nb + u0 > 0) __syncthreads();
+#pragma unroll
+        for (int u = 0; u < C::kMergeU; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            merge[warp * C::kMergeFloats + u * C::kUStride + e * 32 + lane] = acc[nb][u0 + u][e];
+        __syncthreads();
+        // element i: row, 16-dimension piece and place in the piece's part
+        constexpr int kDims = 2 * C::kMergeU;
+#pragma unroll
+        for (int i = tid; i < 64 * kDims; i += kThreads) {
+          const int r = i / (8 * kDims), piece = i / kDims % 8, d = i % kDims, rl = nb * 8 + r;
+          const int row_out = row_info[rl].out;
+          if (row_out < 0) continue;
+          const int gg = (piece & 3) << 1 | piece >> 2;
+          const int at = (d >> 1) * C::kUStride + ((r & 1) + 2 * (d & 1)) * 32 + 4 * gg + (r >> 1);
+          float x = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) x += merge[w * C::kMergeFloats + at];
+          const int dim = 16 * piece + 2 * u0 + d;
           if (whole) {
-            const int i = row / a.group, hg = row - i * a.group;
-            uint16_t* op = static_cast<uint16_t*>(a.out) +
-                           (((static_cast<int64_t>(li) * a.batch + seg.b) * a.n_q + i) * a.hq + h * a.group + hg) * 128 +
-                           16 * pig;
-            const float inv = l[nb][c] == 0.f ? 0.f : 1.f / l[nb][c];
-            uint32_t o[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const float x = acc[nb][u][c] * inv, y = acc[nb][u][2 + c] * inv;
-              if (a.bf16) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-                o[u] = *reinterpret_cast<const uint32_t*>(&v);
-              } else {
-                o[u] = pack_half2(x, y);
-              }
+            x *= l_all[rl];
+            if (a.bf16) {
+              const __nv_bfloat16 v = __float2bfloat16_rn(x);
+              out[row_out + dim] = *reinterpret_cast<const uint16_t*>(&v);
+            } else {
+              out[row_out + dim] = __half_as_ushort(__float2half_rn(x));
             }
-            reinterpret_cast<uint4*>(op)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            reinterpret_cast<uint4*>(op)[1] = make_uint4(o[4], o[5], o[6], o[7]);
           } else {
             // place 0: the segment that opens this CTA's range; 1: a later one
-            float* pp = a.partials + ((static_cast<int64_t>(blockIdx.x) * 2 + (f0 > 0)) * kByteMaxRows + rl) * kBytePartStride;
-            if (g == 0) {
-              pp[0] = m[nb][c];
-              pp[1] = l[nb][c];
-            }
-#pragma unroll
-            for (int u = 0; u < 8; u += 2)
-              *reinterpret_cast<float4*>(pp + 4 + 16 * pig + 2 * u) =
-                  make_float4(acc[nb][u][c], acc[nb][u][2 + c], acc[nb][u + 1][c], acc[nb][u + 1][2 + c]);
+            float* pp = a.partials + ((static_cast<int64_t>(blockIdx.x) * 2 + place) * kByteMaxRows + rl) * kBytePartStride;
+            pp[4 + dim] = x;
+            if (u0 == 0 && i % (8 * kDims) == 0) *reinterpret_cast<float2*>(pp) = make_float2(m_all[rl], l_all[rl]);
           }
         }
-    }
-    f0 += len_seg;
-    if (f0 < mine_total) advance(a, seg, units, len_seg);
+      }
+    __syncthreads();  // row_info and the sums are the next segment's now
   }
   if (dead) {
     if (lane == 0) atomicOr(a.err, kErrTimeout);
@@ -721,101 +857,141 @@ __global__ __launch_bounds__(kThreads, 1) void byte_split_kernel(const __grid_co
 
 // ---- the join ------------------------------------------------------------------
 
-constexpr int kCombThreads = 128;
-constexpr int kCombMaxParts = 1024;  // CTAs of a split pass
+constexpr int kCombAhead = 6;       // parts a warp has on their way at once
 
-// A CTA per (sequence, unit, row): the unit's parts, in the order of their
-// CTAs, joined by their maxima and sums.  Rows of units that one CTA attended
-// whole are done; rows that see nothing become 0.
-__global__ __launch_bounds__(kCombThreads) void byte_combine_kernel(const __grid_constant__ ByteAttnArgs a, int split_grid,
-                                                                    int rows_per_unit) {
-  __shared__ int64_t red[kCombThreads / 32];
-  __shared__ float wgt[kCombMaxParts];
-  __shared__ float accs[kCombThreads / 32][128];
-  __shared__ float fred[kCombThreads / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int units = a.layer_count * a.hkv * a.row_blocks;
-  int id = blockIdx.x;
-  const int rl = id % rows_per_unit;
-  id /= rows_per_unit;
-  const int u = id % units, b = id / units;
-  const int lh = u / a.row_blocks, rb = u - lh * a.row_blocks, li = lh / a.hkv, h = lh - li * a.hkv;
-  const int row = rb * rows_per_unit + rl;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= a.group * a.n_q) return;
-  int64_t sum = 0, before = 0;
-  for (int i = tid; i < a.batch; i += kCombThreads) {
-    const int n = seq_blocks(a, i).n;
-    sum += n;
-    if (i < b) before += n;
+__device__ __forceinline__ void store2(const ByteAttnArgs& a, uint16_t* p, float x, float y) {
+  uint32_t w;
+  if (a.bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    w = *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    w = pack_half2(x, y);
   }
-  const int64_t total = units * block_sum<kCombThreads>(sum, red);
-  before = block_sum<kCombThreads>(before, red);
-  const int n = seq_blocks(a, b).n;
+  *reinterpret_cast<uint32_t*>(p) = w;
+}
+
+// The parts of units that more than one CTA attended, joined by their maxima
+// and sums in the order of the CTAs; rows that see nothing become 0.  WARPS
+// warps share a row's parts (1: units are in few parts, and a CTA's 8 warps
+// take 8 rows; 16: a CTA a row).  What depends on the call's inputs alone is
+// worked out before the split pass has to be over.
+template <int WARPS>
+__global__ __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) void byte_combine_kernel(const __grid_constant__ ByteAttnArgs a,
+                                                                                      int split_grid, int split_warps,
+                                                                                      int rows_per_unit) {
+  constexpr int kThreads = WARPS == 1 ? 256 : 32 * WARPS, kRowsCta = WARPS == 1 ? 8 : 1;
+  __shared__ Sums red[kThreads / 32];
+  __shared__ float accs[WARPS][128];
+  __shared__ float2 ml[WARPS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int units = a.layer_count * a.hkv * a.row_blocks, pad = unit_pad(a);
+  int id = blockIdx.x;
+  const int row_ctas = rows_per_unit / kRowsCta;
+  const int rl = id % row_ctas * kRowsCta + (WARPS == 1 ? warp : 0), slice = WARPS == 1 ? 0 : warp;
+  id /= row_ctas;
+  const int u = id % units, b = id / units;
+  const Unit un = unit_of(a, u);
+  const int row = un.rb * rows_per_unit + rl;
+  const int n = seq_steps(a, b).n;
+  Sums sum{n, n, n > 0}, before{0, 0, 0};
+  if (a.batch > 1) {
+    sum = before;
+    for (int i = tid; i < a.batch; i += kThreads) {
+      const int ni = seq_steps(a, i).n;
+      sum.v += places(ni, pad);
+      sum.r += ni;
+      sum.k += ni > 0;
+      if (i < b) before.v += places(ni, pad);
+    }
+    sum = block_sum<kThreads>(sum, red);
+    before = block_sum<kThreads>(before, red);
+  }
   const int i = row / a.group, hg = row - i * a.group;
   uint16_t* op = static_cast<uint16_t*>(a.out) +
-                 (((static_cast<int64_t>(li) * a.batch + b) * a.n_q + i) * a.hq + h * a.group + hg) * 128;
-  if (n == 0) {
-    op[tid] = 0;
-    return;
+                 (((static_cast<int64_t>(un.li) * a.batch + b) * a.n_q + i) * a.hq + un.h * a.group + hg) * 128 + 4 * lane;
+  const bool work = row < a.group * a.n_q;
+  int c0 = 0, parts = 1, first = 0;
+  if (n > 0) {
+    const int64_t s = before.v * units + static_cast<int64_t>(u) * (n + pad);
+    const Shares sh = shares(sum, units, split_grid, split_warps);
+    c0 = sh.of(s + pad);
+    parts = sh.of(s + pad + n - 1) - c0 + 1;
+    // the unit's place in CTA c0: 0 where no step of another unit comes first
+    first = sh.begin(c0) >= s ? 0 : 1;
   }
-  const int ctas = active_ctas(total, split_grid);
-  const int64_t s = before * units + static_cast<int64_t>(u) * n;
-  const int c0 = cta_of(s, total, ctas), c1 = cta_of(s + n - 1, total, ctas);
-  if (c0 == c1) return;
-  const int parts = c1 - c0 + 1;
-  const int first = static_cast<int64_t>(c0) * total / ctas == s ? 0 : 1;  // the unit's place in CTA c0
-  auto part = [&](int k) {
-    return a.partials + ((static_cast<int64_t>(c0 + k) * 2 + (k == 0 ? first : 0)) * kByteMaxRows + rl) * kBytePartStride;
-  };
-  float mx = -CUDART_INF_F;
-  for (int k = tid; k < parts; k += kCombThreads) {
-    const float m = __ldcg(part(k));
-    wgt[k] = m;
-    mx = fmaxf(mx, m);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) fred[warp] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kCombThreads / 32; ++w) mx = fmaxf(mx, fred[w]);
-  float l = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n == 0 && work && slice == 0) *reinterpret_cast<uint2*>(op) = make_uint2(0u, 0u);
+  if (n == 0 || parts == 1 || (WARPS > 1 && !work)) return;
+  // a warp's parts: slice, slice + WARPS, ..., with the running maximum
+  const float* const part0 = a.partials + (static_cast<int64_t>(c0) * 2 * kByteMaxRows + rl) * kBytePartStride;
+  constexpr int64_t kPart = 2 * kByteMaxRows * kBytePartStride;
+  float m = -CUDART_INF_F, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = warp; k < parts; k += kCombThreads / 32) {
-    const float* pp = part(k);
-    const float m = wgt[k], w = m == mx ? 1.f : ex2(m - mx);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(pp + 4) + lane);
-    l += w * __ldcg(pp + 1);
-    acc.x += w * x.x;
-    acc.y += w * x.y;
-    acc.z += w * x.z;
-    acc.w += w * x.w;
-  }
-  reinterpret_cast<float4*>(accs[warp])[lane] = acc;
-  __syncthreads();
-  if (lane == 0) fred[warp] = l;
-  __syncthreads();
-  float o = 0.f, lt = 0.f;
+  if (work) {
+#pragma unroll 1
+    for (int k0 = slice; k0 < parts; k0 += kCombAhead * WARPS) {
+      float4 x[kCombAhead];
+      float2 s[kCombAhead];
 #pragma unroll
-  for (int w = 0; w < kCombThreads / 32; ++w) {
-    o += accs[w][tid];
-    lt += fred[w];
+      for (int j = 0; j < kCombAhead; ++j) {
+        const int k = k0 + j * WARPS;
+        s[j] = make_float2(-CUDART_INF_F, 0.f);
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < parts) {
+          const float* p = part0 + k * kPart + (k == 0 ? first * kByteMaxRows * kBytePartStride : 0);
+          s[j] = __ldcg(reinterpret_cast<const float2*>(p));
+          x[j] = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
+        }
+      }
+      float mx = m;
+#pragma unroll
+      for (int j = 0; j < kCombAhead; ++j) mx = fmaxf(mx, s[j].x);
+      const float w0 = m == mx ? 1.f : ex2(m - mx);
+      l *= w0;
+      acc = make_float4(acc.x * w0, acc.y * w0, acc.z * w0, acc.w * w0);
+#pragma unroll
+      for (int j = 0; j < kCombAhead; ++j) {
+        const float w = s[j].x == mx ? 1.f : ex2(s[j].x - mx);
+        l = fmaf(w, s[j].y, l);
+        acc = make_float4(fmaf(w, x[j].x, acc.x), fmaf(w, x[j].y, acc.y), fmaf(w, x[j].z, acc.z), fmaf(w, x[j].w, acc.w));
+      }
+      m = mx;
+    }
   }
-  o = lt == 0.f ? 0.f : o / lt;
-  if (a.bf16) {
-    const __nv_bfloat16 v = __float2bfloat16_rn(o);
-    op[tid] = *reinterpret_cast<const uint16_t*>(&v);
+  if constexpr (WARPS == 1) {
+    if (!work) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store2(a, op, acc.x * inv, acc.y * inv);
+    store2(a, op + 2, acc.z * inv, acc.w * inv);
   } else {
-    const __half v = __float2half_rn(o);
-    op[tid] = *reinterpret_cast<const uint16_t*>(&v);
+    reinterpret_cast<float4*>(accs[warp])[lane] = acc;
+    if (lane == 0) ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (tid >= 128) return;
+    float mx = -CUDART_INF_F;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml[w].x);
+    float o = 0.f, lt = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = ml[w].x == mx ? 1.f : ex2(ml[w].x - mx);
+      o = fmaf(f, accs[w][tid], o);
+      lt = fmaf(f, ml[w].y, lt);
+    }
+    o = lt == 0.f ? 0.f : o / lt;
+    op += tid - 4 * lane;
+    if (a.bf16) {
+      const __nv_bfloat16 v = __float2bfloat16_rn(o);
+      *op = *reinterpret_cast<const uint16_t*>(&v);
+    } else {
+      *op = __half_as_ushort(__float2half_rn(o));
+    }
   }
 }
 
 template <int CODE, int NB>
 cudaError_t launch_split(const ByteAttnArgs& a, int grid, cudaStream_t stream) {
-  byte_split_kernel<CODE, NB><<<grid, kThreads, SplitSmem<NB>::kTotal, stream>>>(a);
+  byte_split_kernel<CODE, NB><<<grid, Split<NB>::kThreads, Split<NB>::kTotal, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -826,10 +1002,10 @@ size_t byte_partial_bytes(int n_sms) {
 }
 
 cudaError_t byte_decode_setup() {
-  cudaError_t e = set_smem(byte_split_kernel<0, 1>, SplitSmem<1>::kTotal);
-  if (e == cudaSuccess) e = set_smem(byte_split_kernel<1, 1>, SplitSmem<1>::kTotal);
-  if (e == cudaSuccess) e = set_smem(byte_split_kernel<0, 2>, SplitSmem<2>::kTotal);
-  if (e == cudaSuccess) e = set_smem(byte_split_kernel<1, 2>, SplitSmem<2>::kTotal);
+  cudaError_t e = set_smem(byte_split_kernel<0, 1>, Split<1>::kTotal);
+  if (e == cudaSuccess) e = set_smem(byte_split_kernel<1, 1>, Split<1>::kTotal);
+  if (e == cudaSuccess) e = set_smem(byte_split_kernel<0, 2>, Split<2>::kTotal);
+  if (e == cudaSuccess) e = set_smem(byte_split_kernel<1, 2>, Split<2>::kTotal);
   return e;
 }
 
@@ -840,7 +1016,10 @@ cudaError_t launch_byte_attn(const ByteShape& s, ByteAttnArgs& a, cudaStream_t s
   const int64_t units = static_cast<int64_t>(a.layer_count) * a.hkv * a.row_blocks;
   const int64_t comb = units * a.batch * 8 * nb;
   if (units > INT32_MAX || comb > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const int64_t most = (units * a.batch * s.ntiles + kWarps - 1) / kWarps;
+  // a CTA for each `warps` steps or for each unit (shares())
+  const int warps = nb == 1 ? Split<1>::kWarps : Split<2>::kWarps;
+  const int64_t steps = (s.ntiles * (kByteBlock / kStep) + warps - 1) / warps;
+  const int64_t most = units * a.batch * steps;
   const int grid = static_cast<int>(most < s.n_sms ? most : s.n_sms);
   cudaError_t e;
   if (s.code == 0)
@@ -848,8 +1027,12 @@ cudaError_t launch_byte_attn(const ByteShape& s, ByteAttnArgs& a, cudaStream_t s
   else
     e = nb == 1 ? launch_split<1, 1>(a, grid, stream) : launch_split<1, 2>(a, grid, stream);
   if (e != cudaSuccess) return e;
-  return launch_dependent(byte_combine_kernel, dim3(static_cast<unsigned>(comb)), dim3(kCombThreads), 0, stream, a, grid,
-                          8 * nb);
+  // few units: many parts each, a CTA a row; else a warp a row
+  if (units * a.batch * 8 <= grid)
+    return launch_dependent(byte_combine_kernel<16>, dim3(static_cast<unsigned>(comb)), dim3(512), 0, stream, a, grid, warps,
+                            8 * nb);
+  return launch_dependent(byte_combine_kernel<1>, dim3(static_cast<unsigned>(comb / 8)), dim3(256), 0, stream, a, grid,
+                          warps, 8 * nb);
 }
 
 }  // namespace bgtq
