@@ -243,13 +243,12 @@ def _check(status):
 
 def _ptr(x):
     """Device or host address of a torch tensor / numpy array / int."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    if isinstance(x, np.ndarray):
-        return x.ctypes.data
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return x.ctypes.data if isinstance(x, np.ndarray) else int(x)
 
 
 ERR_INVALID_ARG = -1
@@ -257,9 +256,25 @@ ERR_INVALID_ARG = -1
 
 def _expect(t, name, shape, dtype, device):
     """Raises BgtqError(ERR_INVALID_ARG) unless t is a contiguous torch tensor
-    of dtype on device with this shape (None: any extent).  PackedKVCache
-    checks its tensors this way before a pointer reaches the library, which
+    of dtype on device with this shape (None: any extent).  The caches
+    check their tensors this way before a pointer reaches the library, which
     reads the layouts that include/bgtq.h states."""
+    try:
+        if t.dtype is dtype and t.device == device and t.is_contiguous():
+            have = t.shape
+            if len(have) == len(shape):
+                for e, want in zip(have, shape):
+                    if e != want and want is not None:
+                        break
+                else:
+                    return
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, device)
+
+
+def _refuse(t, name, shape, dtype, device):
+    """What is wrong with t (see _expect): an error, or nothing where only the device's index was left open."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise BgtqError(ERR_INVALID_ARG, f"{name}: a torch tensor is expected")
@@ -274,10 +289,17 @@ def _expect(t, name, shape, dtype, device):
         raise BgtqError(ERR_INVALID_ARG, f"{name}: not contiguous")
 
 
+def _device(device):
+    """torch.device with its index: a state belongs to one GPU."""
+    import torch
+    d = torch.device(device)
+    return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+
+
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())  # of torch.cuda.current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -460,9 +482,12 @@ def bgtq_byte_append(state, layer, layer_count, d_k, d_v, d_start, d_count, batc
 def bgtq_byte_decode_attn(state, layer, layer_count, d_q, d_seq_lens, batch, n_q, d_out, scale=0.0, softcap=0.0,
                           window=0, d_slopes=None, d_prefix=None, d_doc_start=None, stream=None):
     """The score's fields by keyword (bgtq_score)."""
-    score = _Score(scale, softcap, window, 0, _ptr(d_slopes), _ptr(d_prefix), _ptr(d_doc_start))
-    _check(lib().bgtq_byte_decode_attn(state, layer, layer_count, _ptr(d_q), _ptr(d_seq_lens), batch, n_q,
-                                       ctypes.addressof(score), _ptr(d_out), _stream(stream)))
+    score = at = None
+    if scale or softcap or window or d_slopes is not None or d_prefix is not None or d_doc_start is not None:
+        score = _Score(scale, softcap, window, 0, _ptr(d_slopes), _ptr(d_prefix), _ptr(d_doc_start))
+        at = ctypes.addressof(score)
+    _check(lib().bgtq_byte_decode_attn(state, layer, layer_count, _ptr(d_q), _ptr(d_seq_lens), batch, n_q, at,
+                                       _ptr(d_out), _stream(stream)))
 
 
 def bgtq_page_scratch_bytes(state):
@@ -497,10 +522,14 @@ def bgtq_compact_pages(state, d_table, d_refs, d_lens, batch, d_table_out, d_ref
 def bgtq_rope_axes(n_q_heads, n_kv_heads, pairing, dtype, axis, base, d_q, q_stride, d_k, k_stride, d_pos, n_axes,
                    tokens, d_q_out, q_out_stride, d_k_out, k_out_stride, head_dim=HEAD_DIM, stream=None):
     """The config's fields first (bgtq_rope_config); axis: 64 integers."""
-    if len(axis) != N_BLOCKS or any(int(x) != x or not 0 <= x < 256 for x in axis):
+    try:
+        raw = bytes(axis)
+    except (TypeError, ValueError):
+        raw = b""
+    if len(raw) != N_BLOCKS:
         raise BgtqError(ERR_INVALID_ARG, f"axis: expected {N_BLOCKS} axis numbers")
-    c = _RopeConfig(n_q_heads, n_kv_heads, head_dim, pairing, dtype, n_axes, (ctypes.c_uint8 * N_BLOCKS)(*map(int, axis)),
-                    float(base))
+    c = _RopeConfig(n_q_heads, n_kv_heads, head_dim, pairing, dtype, n_axes,
+                    (ctypes.c_uint8 * N_BLOCKS).from_buffer_copy(raw), float(base))
     _check(lib().bgtq_rope_axes(ctypes.byref(c), _ptr(d_q), q_stride, _ptr(d_k), k_stride, _ptr(d_pos), tokens,
                                 _ptr(d_q_out), q_out_stride, _ptr(d_k_out), k_out_stride, _stream(stream)))
 
@@ -525,24 +554,26 @@ def rope_axes(q, k, pos, axis, base, q_out=None, k_out=None, pairing=0):
     Returns (q_out, k_out).
     """
     import torch
-    if q is None and k is None:
-        raise BgtqError(ERR_INVALID_ARG, "q, k: one of them is needed")
     one = k if q is None else q
     if not isinstance(one, torch.Tensor) or one.dtype not in (torch.float16, torch.bfloat16) or one.dim() != 3:
-        raise BgtqError(ERR_INVALID_ARG, "q, k: fp16 or bf16 tensors [tokens, heads, 128] are expected")
+        raise BgtqError(ERR_INVALID_ARG, "q, k: one of them is needed, fp16 or bf16 [tokens, heads, 128]")
     tokens, dev = one.shape[0], one.device
 
     def rows(t, name, heads):
+        """(heads, elements from a token to the next)"""
         if t is None:
             return 0, 0
-        _expect(t[:1].contiguous() if isinstance(t, torch.Tensor) and t.dim() == 3 else t, name,
-                (min(1, tokens), heads, HEAD_DIM), one.dtype, dev)
-        if (t.shape[0] != tokens or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != HEAD_DIM) or
-                t.stride(0) >= 1 << 31 or tokens >= 1 << 31):
-            raise BgtqError(ERR_INVALID_ARG, f"{name}: {tuple(t.shape)}, strides {t.stride()}: expected {tokens} tokens "
-                                             "of contiguous heads")
-        # a single token has no next one: its stride says nothing
-        return t.shape[1], t.stride(0) if tokens > 1 else t.shape[1] * HEAD_DIM
+        if not isinstance(t, torch.Tensor) or t.dtype != one.dtype or t.device != dev or t.dim() != 3:
+            raise BgtqError(ERR_INVALID_ARG, f"{name}: a tensor [tokens, heads, 128] of {one.dtype} on {dev} is expected")
+        (n, h, d), (sn, sh, sd) = t.shape, t.stride()
+        if n != tokens or d != HEAD_DIM or (heads is not None and h != heads) or n >= 1 << 31:
+            raise BgtqError(ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)}, expected "
+                                             f"{(tokens, '*' if heads is None else heads, HEAD_DIM)}")
+        if n == 1 or n == 0:
+            sn = h * HEAD_DIM   # there is no next token
+        if sd != 1 or (h > 1 and sh != HEAD_DIM) or sn >= 1 << 31:
+            raise BgtqError(ERR_INVALID_ARG, f"{name}: strides {t.stride()}, expected contiguous heads")
+        return h, sn
 
     hq, sq = rows(q, "q", None)
     hkv, sk = rows(k, "k", None)
@@ -554,8 +585,10 @@ def rope_axes(q, k, pos, axis, base, q_out=None, k_out=None, pairing=0):
         raise BgtqError(ERR_INVALID_ARG, "q_out, k_out: given without q, k")
     sqo, sko = rows(q_out, "q_out", hq)[1], rows(k_out, "k_out", hkv)[1]
     _expect(pos, "pos", (None, tokens), torch.int32, dev)
-    if dev.type == "cuda" and torch.cuda.current_device() != dev.index:
-        raise BgtqError(ERR_INVALID_ARG, f"q, k: on {dev}, which is not the current device")
+    if len(axis) != N_BLOCKS:
+        raise BgtqError(ERR_INVALID_ARG, f"axis: expected {N_BLOCKS} axis numbers")
+    if dev.type != "cuda" or torch.cuda.current_device() != dev.index:
+        raise BgtqError(ERR_INVALID_ARG, f"q, k: on {dev}, which is not the current GPU")
     if tokens > 0:
         bgtq_rope_axes(hq, hkv, pairing, 1 if one.dtype == torch.bfloat16 else 0, axis, base, q, sq, k, sk, pos,
                        pos.shape[0], tokens, q_out, sqo, k_out, sko)
@@ -632,7 +665,7 @@ class PackedKVCache(_Pages):
     def __init__(self, cfg, device="cuda"):
         import torch
         self.cfg = cfg
-        self.device = torch.device(device)
+        self.device = _device(device)
         self.cache_bytes, self.workspace_bytes = bgtq_required_bytes(cfg)
         self.cache = torch.zeros(self.cache_bytes, dtype=torch.uint8, device=self.device)
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
@@ -873,7 +906,7 @@ class ByteKVCache(_Pages):
     def __init__(self, cfg, device="cuda"):
         import torch
         self.cfg = cfg
-        self.device = torch.device(device)
+        self.device = _device(device)
         self.cache_bytes, self.workspace_bytes = bgtq_byte_required_bytes(cfg)
         self.cache = torch.zeros(self.cache_bytes, dtype=torch.uint8, device=self.device)
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)

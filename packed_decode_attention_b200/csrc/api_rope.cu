@@ -74,8 +74,14 @@ extern "C" int bgtq_rope_axes(const bgtq_rope_config* cfg, const void* d_q, int3
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return BGTQ_ERR_CUDA;
   bgtq::RopeAxesArgs a;
   std::memset(&a, 0, sizeof(a));
+  // base^(-j/64) = base^(-(j/8)/8) base^(-(j%8)/64)
+  double hi[8], lo[8];
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = std::pow(cfg->base, -i / 8.0) / 6.283185307179586477;
+    lo[i] = std::pow(cfg->base, -i / 64.0);
+  }
   for (int j = 0; j < 64; ++j) {
-    a.turns[j] = std::pow(cfg->base, -2.0 * j / bgtq::kD) / 6.283185307179586477;
+    a.turns[j] = hi[j >> 3] * lo[j & 7];
     a.axis[j] = cfg->axis[j];
   }
   a.pos = d_pos;

@@ -57,6 +57,46 @@ __device__ __forceinline__ float2 decode2(uint32_t w, int code) {
   return make_float2(static_cast<float>(static_cast<int8_t>(w & 255)), static_cast<float>(static_cast<int8_t>(w >> 8 & 255)));
 }
 
+// Two finite elements of a row, scaled by 2^-e, to two e4m3 codes.  Products
+// by a power of two are exact in fp16 (INV: its pair, -15 <= e <= 15) and in
+// bf16 but for what lies far under e4m3's least step of 2^-9, which is 0
+// either way.
+template <bool BF16>
+__device__ __forceinline__ uint32_t scale2_e4m3(uint32_t w, uint32_t inv) {
+  uint16_t r;
+  if constexpr (BF16) {
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&w), *reinterpret_cast<__nv_bfloat162*>(&inv));
+    const uint32_t y = *reinterpret_cast<const uint32_t*>(&x);
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(r)
+        : "f"(__uint_as_float(y & 0xFFFF0000u)), "f"(__uint_as_float(y << 16)));
+  } else {
+    const __half2 x = __hmul2(*reinterpret_cast<__half2*>(&w), *reinterpret_cast<__half2*>(&inv));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  }
+  return r;
+}
+
+// Four finite elements to four int8 codes: adding 1.5 times the number whose
+// last place is 1 rounds to an integer, to nearest even, in the low bits
+// (|x 2^-e| <= 127, and the product is exact inside the fused operation).
+template <bool BF16>
+__device__ __forceinline__ uint32_t scale4_int8(uint32_t w0, uint32_t w1, float inv, uint32_t inv2) {
+  if constexpr (BF16) {
+    const float m = 12582912.f;  // 1.5 2^23
+    const uint32_t a = __float_as_uint(fmaf(__uint_as_float(w0 << 16), inv, m));
+    const uint32_t b = __float_as_uint(fmaf(__uint_as_float(w0 & 0xFFFF0000u), inv, m));
+    const uint32_t c = __float_as_uint(fmaf(__uint_as_float(w1 << 16), inv, m));
+    const uint32_t d = __float_as_uint(fmaf(__uint_as_float(w1 & 0xFFFF0000u), inv, m));
+    return prmt(prmt(a, b, 0x0040u), prmt(c, d, 0x0040u), 0x5410u);
+  } else {
+    const __half2 m = __half2half2(__ushort_as_half(0x6600));  // 1.5 2^10
+    const __half2 k = *reinterpret_cast<__half2*>(&inv2);
+    const __half2 a = __hfma2(*reinterpret_cast<__half2*>(&w0), k, m), b = __hfma2(*reinterpret_cast<__half2*>(&w1), k, m);
+    return prmt(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b), 0x6420u);
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ float2 row2(uint32_t w) {
   if constexpr (BF16) return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
@@ -68,10 +108,11 @@ __device__ __forceinline__ float2 row2(uint32_t w) {
 // heads.  Thread (r, c) of the 16 x 16 holds dimensions 8 c .. 8 c + 7 of
 // rows r, r + 16, r + 32, r + 48: 64 bytes in flight a thread, and a row's
 // 256 bytes are one warp half's load.  Bound by HBM: 2 bytes read and 1
-// written an element; the conversion is about a third of that time's issue
-// slots.
-template <bool BF16>
-__global__ __launch_bounds__(kAppThreads) void byte_append_kernel(ByteShape sh, ByteCacheDev cache,
+// written an element.  Magnitudes are compared as packed 16-bit integers,
+// and finite rows of an ordinary size are converted two elements at a time;
+// other rows take the path through fp32, element by element.
+template <bool BF16, int CODE>
+__global__ __launch_bounds__(kAppThreads, 5) void byte_append_kernel(ByteShape sh, ByteCacheDev cache,
                                                                   const int32_t* __restrict__ table, uint32_t* err,
                                                                   int layer0, const uint16_t* __restrict__ k,
                                                                   const uint16_t* __restrict__ v,
@@ -79,14 +120,15 @@ __global__ __launch_bounds__(kAppThreads) void byte_append_kernel(ByteShape sh, 
                                                                   const int32_t* __restrict__ count_v, int batch, int n,
                                                                   int blocks_per_seq) {
   const int tid = threadIdx.x;
-  int64_t id = blockIdx.x;
-  const int h = id % sh.n_kv_heads;
-  id /= sh.n_kv_heads;
+  uint32_t id = blockIdx.x;
+  const uint32_t heads = sh.n_kv_heads;
+  const int h = id % heads;
+  id /= heads;
   const int kind = id & 1;
   id >>= 1;
-  const int tb = id % blocks_per_seq;
-  id /= blocks_per_seq;
-  const int b = id % batch, li = id / batch;
+  const int tb = id % static_cast<uint32_t>(blocks_per_seq);
+  id /= static_cast<uint32_t>(blocks_per_seq);
+  const int b = id % static_cast<uint32_t>(batch), li = id / static_cast<uint32_t>(batch);
   const int layer = layer0 + li;
   const int start = start_v[b], count = count_v[b];
   if (start < 0 || count < 0 || count > n) {
@@ -129,28 +171,47 @@ __global__ __launch_bounds__(kAppThreads) void byte_append_kernel(ByteShape sh, 
     w[s] = p >= lo && p < hi ? __ldcs(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(p) * sh.n_kv_heads * 128))
                              : make_uint4(0u, 0u, 0u, 0u);
   }
-  float amax = 0.f;
-  bool bad = false;
+  // the magnitudes' bits order as the magnitudes do; kInf and above: not finite
+  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+  __shared__ uint32_t red[kAppThreads / 32];
+  auto largest = [&](uint32_t x) {
+    const uint32_t wm = __reduce_max_sync(0xffffffffu, x);
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = wm;
+    __syncthreads();
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kAppThreads / 32; ++i) m = max(m, red[i]);
+    return m;
+  };
+  uint32_t pair = 0;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const uint32_t u[4] = {w[s].x, w[s].y, w[s].z, w[s].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = row2<BF16>(u[j]);
-      const float a = fabsf(f.x), d = fabsf(f.y);
-      if (a < CUDART_INF_F) amax = fmaxf(amax, a); else bad = true;
-      if (d < CUDART_INF_F) amax = fmaxf(amax, d); else bad = true;
-    }
+    for (int j = 0; j < 4; ++j) pair = __vmaxu2(pair, u[j] & 0x7FFF7FFFu);
   }
-  __shared__ uint32_t red[kAppThreads / 32];
-  const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-  if ((tid & 31) == 0) red[tid >> 5] = wm;
-  if (bad) atomicOr(err, kErrNonFinite);
-  __syncthreads();
-  uint32_t m = 0;
+  uint32_t m = largest(max(pair & 0xFFFFu, pair >> 16));
+  const bool finite = m < kInf;
+  if (!finite) {
+    // the largest finite one
+    uint32_t x = 0;
+    bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kAppThreads / 32; ++i) m = max(m, red[i]);
-  int e = block_exp(__uint_as_float(m), sh.code);
+    for (int s = 0; s < 4; ++s) {
+      const uint32_t u[4] = {w[s].x, w[s].y, w[s].z, w[s].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = u[j] & 0x7FFFu, d = u[j] >> 16 & 0x7FFFu;
+        if (a < kInf) x = max(x, a); else bad = true;
+        if (d < kInf) x = max(x, d); else bad = true;
+      }
+    }
+    if (bad) atomicOr(err, kErrNonFinite);
+    m = largest(x);
+  }
+  m = __float_as_uint(row2<BF16>(m).x);
+  int e = block_exp(__uint_as_float(m), CODE);
   int grow = 0;  // e - e_old where the block's other codes are to be rescaled
   if (lo > 0) {
     // a block nothing was written to has no power of two in its place: as the least scale
@@ -160,25 +221,39 @@ __global__ __launch_bounds__(kAppThreads) void byte_append_kernel(ByteShape sh, 
     else e = e_old;
   }
   const float inv = pow2(-e);
+  // 2^-e as a pair of the rows' type; fp16 has it for -15 <= e <= 15
+  const bool packed = finite && (BF16 || (e >= -15 && e <= 15));
+  uint32_t inv2;
+  if constexpr (BF16)
+    inv2 = (__float_as_uint(inv) & 0xFFFF0000u) | __float_as_uint(inv) >> 16;
+  else
+    inv2 = pack_half2(inv, inv);
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int p = r + 16 * s;
     uint2* at = reinterpret_cast<uint2*>(codes + p * 128 + 8 * c);
     uint32_t out[4];
-    if (p >= lo && p < hi) {
+    if (p >= lo && p < hi && packed) {
+      if constexpr (CODE == 0)
+        *at = make_uint2(scale2_e4m3<BF16>(w[s].x, inv2) | scale2_e4m3<BF16>(w[s].y, inv2) << 16,
+                         scale2_e4m3<BF16>(w[s].z, inv2) | scale2_e4m3<BF16>(w[s].w, inv2) << 16);
+      else
+        *at = make_uint2(scale4_int8<BF16>(w[s].x, w[s].y, inv, inv2), scale4_int8<BF16>(w[s].z, w[s].w, inv, inv2));
+      continue;
+    } else if (p >= lo && p < hi) {
       const uint32_t u[4] = {w[s].x, w[s].y, w[s].z, w[s].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = row2<BF16>(u[j]);
-        out[j] = encode2(f.x * inv, f.y * inv, sh.code);
+        out[j] = encode2(f.x * inv, f.y * inv, CODE);
       }
     } else if (grow > 0) {
       const uint2 was = *at;
       const float down = grow > 126 ? 0.f : pow2(-grow);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 f = decode2((j < 2 ? was.x : was.y) >> (16 * (j & 1)) & 0xFFFFu, sh.code);
-        out[j] = encode2(f.x * down, f.y * down, sh.code);
+        const float2 f = decode2((j < 2 ? was.x : was.y) >> (16 * (j & 1)) & 0xFFFFu, CODE);
+        out[j] = encode2(f.x * down, f.y * down, CODE);
       }
     } else {
       continue;
@@ -199,12 +274,14 @@ cudaError_t launch_byte_append(const ByteShape& s, const ByteCacheDev& c, const 
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   const uint16_t* kp = static_cast<const uint16_t*>(k);
   const uint16_t* vp = static_cast<const uint16_t*>(v);
-  if (s.bf16)
-    byte_append_kernel<true><<<static_cast<unsigned>(ctas), kAppThreads, 0, stream>>>(
-        s, c, block_table, err, layer0, kp, vp, start, count, batch, n, per_seq);
+  auto launch = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(ctas), kAppThreads, 0, stream>>>(s, c, block_table, err, layer0, kp, vp, start, count,
+                                                                    batch, n, per_seq);
+  };
+  if (s.code == 0)
+    s.bf16 ? launch(byte_append_kernel<true, 0>) : launch(byte_append_kernel<false, 0>);
   else
-    byte_append_kernel<false><<<static_cast<unsigned>(ctas), kAppThreads, 0, stream>>>(
-        s, c, block_table, err, layer0, kp, vp, start, count, batch, n, per_seq);
+    s.bf16 ? launch(byte_append_kernel<true, 1>) : launch(byte_append_kernel<false, 1>);
   return cudaGetLastError();
 }
 

@@ -26,7 +26,7 @@ constexpr float kPShift = 14.f;          // softmax weights are held as 2^14 p (
 // A unit (one KV head's rows of one sequence) costs a CTA its queries and a
 // merge besides its steps: about as long as this many steps.  Counted when
 // the work is shared out, so that a CTA gets few short sequences.
-constexpr int kUnitCost = 12;
+constexpr int kUnitCost = 18;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -25,7 +25,7 @@ def sections(n_axes):
 
 def check(x, got, pos, axis, base, pairing):
     """Sines: the angle's fraction in fp32 (2^-25 turns: 2^-22 in the sine), its sine's own rounding (2^-23), two
-    products and a difference (2^-23 in all): 2^-21 of |a| + |b|.  The angle in fp64: four roundings of the turns
+    products and a difference (2^-23 in all): 2^-21 of |a| + |b|.  The angle in fp64: five roundings of the turns
     here, one of the angle in the oracle, 2^-50 of the angle.  Then the output's rounding."""
     n, heads = x.shape[0], x.shape[1]
     xd, gd, pn = x.double().cpu().numpy(), got.double().cpu().numpy(), pos.cpu().numpy()
