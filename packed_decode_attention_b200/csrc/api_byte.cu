@@ -23,7 +23,7 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 struct ByteLayout {
   size_t codes[2], scales[2], cache_total;
-  size_t err, partials, ws_total;
+  size_t err, partials, parts, ws_total;
 };
 
 int64_t blocks_of(int64_t capacity) { return (capacity + bgtq::kByteBlock - 1) / bgtq::kByteBlock; }
@@ -47,6 +47,9 @@ int validate(const bgtq_byte_config* c) {
   if (c->capacity_tokens < 1 || c->capacity_tokens > (int64_t(1) << 30)) return BGTQ_ERR_INVALID_ARG;
   // the codes' rows of 128 bytes are addressed by an int32 coordinate
   if (slots_estimate(c) * bgtq::kByteBlock > 2147483648.0 - bgtq::kByteBlock) return BGTQ_ERR_INVALID_ARG;
+  // the workspace's places for each unit of a call
+  if (double(c->n_layers) * c->n_q_heads * c->max_q_tokens * double(c->max_batch) > 1125899906842624.0)  // 2^50
+    return BGTQ_ERR_INVALID_ARG;
   return BGTQ_OK;
 }
 
@@ -70,7 +73,9 @@ ByteLayout plan(const bgtq_byte_config* c) {
   p.cache_total = align_up(p.scales[1] + slots * sizeof(float));
   p.err = 0;
   p.partials = kAlign;
-  p.ws_total = align_up(p.partials + bgtq::byte_partial_bytes(kMaxSplitCtas));
+  p.parts = align_up(p.partials + bgtq::byte_partial_bytes(kMaxSplitCtas));
+  p.ws_total = align_up(p.parts + bgtq::byte_parts_bytes(c->n_layers, c->n_kv_heads, c->n_q_heads / c->n_kv_heads,
+                                                         c->max_batch, c->max_q_tokens));
   return p;
 }
 
@@ -167,6 +172,7 @@ int bgtq_byte_create(const bgtq_byte_config* cfg, void* d_cache, size_t cache_by
   st->ws_bytes = p.ws_total;
   st->ws.err = reinterpret_cast<uint32_t*>(w8 + p.err);
   st->byte_partials = reinterpret_cast<float*>(w8 + p.partials);
+  st->byte_parts = reinterpret_cast<int2*>(w8 + p.parts);
   bgtq::ByteShape& s = st->byte_shape;
   s.n_layers = cfg->n_layers;
   s.n_kv_heads = cfg->n_kv_heads;
@@ -243,6 +249,7 @@ int bgtq_byte_decode_attn(bgtq_state* st, int32_t layer, int32_t layer_count, co
   a.out = d_out;
   a.seq_lens = d_seq_lens;
   a.partials = st->byte_partials;
+  a.parts = st->byte_parts;
   a.err = st->ws.err;
   a.capacity = s.capacity;
   a.ntiles = s.ntiles;

@@ -41,6 +41,7 @@ struct ByteAttnArgs {
   const int32_t* doc_start;       // [batch][n_q]; null: 0
   const float* slopes;            // [n_q_heads]; null: no bias
   float* partials;
+  int2* parts;                    // of each unit with steps: the place of the first, and how many
   uint32_t* err;
   int64_t capacity, ntiles;
   int32_t n_pages, max_batch, hkv, hq, group, n_q, layer0, layer_count, batch;
@@ -50,7 +51,8 @@ struct ByteAttnArgs {
   float cap;                      // 0: none
 };
 
-// Bytes of the split pass's partials (two a CTA).
+// Bytes of the units' parts, and of the split pass's partials (two a CTA).
+size_t byte_parts_bytes(int n_layers, int n_kv_heads, int group, int max_batch, int max_q_tokens);
 size_t byte_partial_bytes(int n_sms);
 // Sets the kernels' shared-memory limits on the current device.
 cudaError_t byte_decode_setup();

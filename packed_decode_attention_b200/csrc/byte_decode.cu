@@ -286,6 +286,27 @@ __device__ __forceinline__ int slot_of(const ByteAttnArgs& a, const Cursor& c, i
   return c.base + page;
 }
 
+// The end r1 of a CTA's places, in the sequence whose places start at v0 and
+// whose steps start at number s0, n of them a unit: the number of the first
+// step behind the end, and in how many CTAs the unit is that the end cuts
+// (1: none).
+__device__ __forceinline__ void tail_of(const Shares& sh, int64_t v0, int64_t s0, int64_t r1, int n, int pad, int64_t& end,
+                                        int& tail) {
+  const int np = places(n, pad);
+  const int64_t u = quot(r1 - v0, np), at = v0 + u * np;
+  end = s0 + u * n + max(static_cast<int64_t>(0), r1 - at - pad);
+  tail = r1 > at + pad ? sh.of(at + np - 1) - static_cast<int>(blockIdx.x) + 1 : 1;
+}
+
+// The first step of a CTA, `off` places into its first sequence, and the
+// number of its steps; `left`: from the sequence's first step to the CTA's end.
+__device__ __forceinline__ void start_of(int64_t off, int64_t left, int pad, Cursor& seg, int& total) {
+  const int np = places(seg.s.n, pad);
+  seg.u = static_cast<int>(quot(off, np));
+  seg.j = max(0, static_cast<int>(off - static_cast<int64_t>(seg.u) * np) - pad);
+  total = static_cast<int>(left - static_cast<int64_t>(seg.u) * seg.s.n - seg.j);
+}
+
 // NB blocks of 8 query rows.  One: 12 warps of 168 registers, two pairs of
 // buffers each (a step's K and V); two, with twice the accumulators: 8 warps
 // of 255, three pairs.
@@ -337,6 +358,7 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
   __shared__ Row row_info[C::kRows];
   __shared__ float ms[kWarps * C::kRows], ls[kWarps * C::kRows], m_all[C::kRows], l_all[C::kRows];
   __shared__ Sums red[kWarps];
+  __shared__ int tail_parts;
   __shared__ int64_t found[4];     // the first sequence, its first place, its first step's number; the end's step
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(&a.map[tid]) : "memory");
@@ -349,31 +371,75 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
   __syncwarp();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // this CTA's places [r0, r1), and the steps among them
+  // this CTA's places [r0, r1), and the steps among them; and for the join, in
+  // how many CTAs the unit is that the CTA ends in
   const int units = a.layer_count * a.hkv * a.row_blocks, pad = unit_pad(a);
   Cursor seg;      // the start of the segment (a unit's steps in this CTA)
   int mine_total;
   if (a.batch == 1) {
     seg.b = 0;
     seg.s = seq_steps(a, 0);
+    const int n = seg.s.n;
     if (seg.s.bad && blockIdx.x == 0 && tid == 0) atomicOr(a.err, kErrSeqLen);
-    if (seg.s.n == 0) return;
-    const Shares sh = shares(Sums{seg.s.n, seg.s.n, 1}, units, gridDim.x, kWarps);
+    if (n == 0) return;
+    const Shares sh = shares(Sums{n, n, 1}, units, gridDim.x, kWarps);
     if (static_cast<int>(blockIdx.x) >= sh.ctas) return;
-    const int64_t r0 = sh.begin(blockIdx.x);
-    seg.u = static_cast<int>(quot(r0, seg.s.n));
-    seg.j = static_cast<int>(r0 - static_cast<int64_t>(seg.u) * seg.s.n);
-    mine_total = static_cast<int>(sh.begin(blockIdx.x + 1) - r0);
+    const int64_t r0 = sh.begin(blockIdx.x), r1 = sh.begin(blockIdx.x + 1);
+    seg.u = static_cast<int>(quot(r0, n));
+    seg.j = static_cast<int>(r0 - static_cast<int64_t>(seg.u) * n);
+    mine_total = static_cast<int>(r1 - r0);
+    if (tid == 0) tail_parts = sh.per > 0 ? sh.per : sh.of((quot(r1 - 1, n) + 1) * n - 1) - static_cast<int>(blockIdx.x) + 1;
+  } else if (a.batch <= 32) {
+    // a lane a sequence, every warp for itself; sums of 32 fit an int32 (a
+    // sequence has fewer than 2^26 places)
+    SeqSteps s{};
+    if (lane < a.batch) s = seq_steps(a, lane);
+    if (s.bad && blockIdx.x == 0 && warp == 0) atomicOr(a.err, kErrSeqLen);
+    const int np = places(s.n, pad);
+    int iv = np, ir = s.n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, iv, o), z = __shfl_up_sync(0xffffffffu, ir, o);
+      if (lane >= o) {
+        iv += y;
+        ir += z;
+      }
+    }
+    const Sums sum{__shfl_sync(0xffffffffu, iv, a.batch - 1), __shfl_sync(0xffffffffu, ir, a.batch - 1),
+                   __popc(__ballot_sync(0xffffffffu, s.n > 0))};
+    if (sum.r == 0) return;
+    const Shares sh = shares(sum, units, gridDim.x, kWarps);
+    if (static_cast<int>(blockIdx.x) >= sh.ctas) return;
+    const int64_t r0 = sh.begin(blockIdx.x), r1 = sh.begin(blockIdx.x + 1);
+    const int64_t v0 = static_cast<int64_t>(iv - np) * units, v1 = static_cast<int64_t>(iv) * units;
+    const int64_t s0 = static_cast<int64_t>(ir - s.n) * units;
+    int64_t end = units * sum.r;
+    int tail = 1;
+    const int last = __ffs(__ballot_sync(0xffffffffu, v0 <= r1 && r1 < v1)) - 1;
+    if (lane == last) tail_of(sh, v0, s0, r1, s.n, pad, end, tail);
+    if (last >= 0) {
+      end = __shfl_sync(0xffffffffu, end, last);
+      tail = __shfl_sync(0xffffffffu, tail, last);
+    }
+    if (tid == 0) tail_parts = tail;
+    seg.b = __ffs(__ballot_sync(0xffffffffu, v0 <= r0 && r0 < v1)) - 1;
+    seg.s.len = __shfl_sync(0xffffffffu, s.len, seg.b);
+    seg.s.pre = __shfl_sync(0xffffffffu, s.pre, seg.b);
+    seg.s.n_pre = __shfl_sync(0xffffffffu, s.n_pre, seg.b);
+    seg.s.t0 = __shfl_sync(0xffffffffu, s.t0, seg.b);
+    seg.s.n = __shfl_sync(0xffffffffu, s.n, seg.b);
+    start_of(r0 - __shfl_sync(0xffffffffu, v0, seg.b), end - __shfl_sync(0xffffffffu, s0, seg.b), pad, seg, mine_total);
   } else {
     int n0 = 0;
     Sums sum{0, 0, 0};
     for (int b = tid; b < a.batch; b += kThreads) {
       const SeqSteps s = seq_steps(a, b);
-      if (b == tid) n0 = s.n;
+      const int n = s.n;
+      if (b == tid) n0 = n;
       if (s.bad && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
-      sum.v += places(s.n, pad);
-      sum.r += s.n;
-      sum.k += s.n > 0;
+      sum.v += places(n, pad);
+      sum.r += n;
+      sum.k += n > 0;
     }
     sum = block_sum<kThreads>(sum, red);
     if (sum.r == 0) return;
@@ -381,11 +447,13 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
     if (static_cast<int>(blockIdx.x) >= sh.ctas) return;
     const int64_t r0 = sh.begin(blockIdx.x), r1 = sh.begin(blockIdx.x + 1);
     Sums before{0, 0, 0};  // of the sequences before this chunk
-    if (tid == 0) found[3] = units * sum.r;
+    if (tid == 0) {
+      found[3] = units * sum.r;
+      tail_parts = 1;
+    }
     for (int base = 0; base < a.batch; base += kThreads) {
       const int b = base + tid;
       const int n = b < a.batch ? (base == 0 ? n0 : seq_steps(a, b).n) : 0, np = places(n, pad);
-      // a sequence has fewer than 2^26 places, so 32 of them fit an int32
       int iv = np, ir = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -415,21 +483,20 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
         found[2] = s0;
       }
       if (v0 <= r1 && r1 < v1) {
-        const int64_t off = r1 - v0, u = quot(off, np);
-        found[3] = s0 + u * n + max(static_cast<int64_t>(0), off - u * np - pad);
+        int64_t end;
+        int tail;
+        tail_of(sh, v0, s0, r1, n, pad, end, tail);
+        found[3] = end;
+        tail_parts = tail;
       }
       if (before.v * units > r1) break;
     }
     __syncthreads();
     seg.b = static_cast<int>(found[0]);
     seg.s = seq_steps(a, seg.b);
-    const int64_t off = r0 - found[1];
-    const int np = places(seg.s.n, pad);
-    seg.u = static_cast<int>(quot(off, np));
-    seg.j = max(0, static_cast<int>(off - static_cast<int64_t>(seg.u) * np) - pad);
-    mine_total = static_cast<int>(found[3] - found[2] - static_cast<int64_t>(seg.u) * seg.s.n - seg.j);
-    if (mine_total <= 0) return;
+    start_of(r0 - found[1], found[3] - found[2], pad, seg, mine_total);
   }
+  if (mine_total <= 0) return;
   seg.base = base_of(a, seg.b, seg.u);
 
   // this warp's steps: warp, warp + kWarps, ... of the CTA's, kRing of them on
@@ -574,7 +641,10 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
           phases ^= 1u << buf;
           pending &= ~(1u << buf);
         } else {
+          // copies on their way land (bounded) before their places are used otherwise
           dead = true;
+          for (int i = 0; i < kRing; ++i)
+            if (pending >> i & 1) bar_wait(bar0 + 8 * i, phases >> i & 1);
         }
       }
       if (!dead) {
@@ -664,12 +734,14 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e & 1] = fmaxf(mx[e & 1], S[nb][mt][e]);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-          }
+          // past the first steps a new maximum is rare: only then do the lanes
+          // agree on it
           if (__any_sync(0xffffffffu, mx[0] != m[nb][0] || mx[1] != m[nb][1])) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+              mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+            }
             // a row nothing of which was visible has m = -inf and acc = l = 0
             const float al[2] = {mx[0] == m[nb][0] ? 1.f : ex2(m[nb][0] - mx[0]),
                                  mx[1] == m[nb][1] ? 1.f : ex2(m[nb][1] - mx[1])};
@@ -685,8 +757,8 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
           // weights 2^14 2^(x - m) in fp16: the tensor cores' type, rounded
           // once (2^-11 relative); the factor keeps weights down to 2^-28 of
           // the largest out of fp16's subnormals, and cancels in acc / l
-          const float s0 = mx[0] == -CUDART_INF_F ? 0.f : kPShift - mx[0];
-          const float s1 = mx[1] == -CUDART_INF_F ? 0.f : kPShift - mx[1];
+          const float s0 = m[nb][0] == -CUDART_INF_F ? 0.f : kPShift - m[nb][0];
+          const float s1 = m[nb][1] == -CUDART_INF_F ? 0.f : kPShift - m[nb][1];
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -755,18 +827,22 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
     }
 
     const bool whole = seg.j == 0 && len_seg == seg.s.n;
-    const int place = f0 > 0;
+    // place 0: the segment that opens this CTA's range; 1: a later one
+    const int place = 2 * blockIdx.x + (f0 > 0);
+    if (seg.j == 0 && tid == 0)
+      a.parts[static_cast<int64_t>(seg.b) * units + seg.u] = make_int2(place, whole ? 1 : tail_parts);
     uint16_t* const out = static_cast<uint16_t*>(a.out) +
                           (static_cast<int64_t>(unit_of(a, seg.u).li) * a.batch + seg.b) * a.n_q * a.hq * 128;
     f0 += len_seg;
-    if (f0 < mine_total) {
+    const bool more = f0 < mine_total;
+    if (more) {
       advance(a, seg, units, len_seg);
       asked = ask(seg);
     }
 
-    // merge of the warps: their maxima and sums, then the accumulators by
-    // parts through shared memory, a thread summing its elements over the
-    // warps in order
+    // merge of the warps: their maxima and sums, then the accumulators
+    // through shared memory, half a row block at a time, a thread summing its
+    // elements over the warps in order
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -779,31 +855,29 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
         }
       }
     __syncthreads();
+    {
+      const int rl = lane % C::kRows;
+      float mw[kWarps], mx = -CUDART_INF_F;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float al[2];
+      for (int w = 0; w < kWarps; ++w) mw[w] = ms[w * C::kRows + rl];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int rl = nb * 8 + 2 * t + c;
-        float mx = -CUDART_INF_F;
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, mw[w]);
+      const float own = ms[warp * C::kRows + rl], f = own == mx ? 1.f : ex2(own - mx);
+      if (warp == 0 && lane < C::kRows) {
+        float sum_l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ms[w * C::kRows + rl]);
-        al[c] = m[nb][c] == mx ? 1.f : ex2(m[nb][c] - mx);
-        if (warp == 0 && g == 0) {
-          float sum_l = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float mw = ms[w * C::kRows + rl];
-            sum_l += ls[w * C::kRows + rl] * (mw == mx ? 1.f : ex2(mw - mx));
-          }
-          m_all[rl] = mx;
-          l_all[rl] = !whole ? sum_l : sum_l == 0.f ? 0.f : 1.f / sum_l;
-        }
+        for (int w = 0; w < kWarps; ++w) sum_l += ls[w * C::kRows + rl] * (mw[w] == mx ? 1.f : ex2(mw[w] - mx));
+        m_all[rl] = mx;
+        l_all[rl] = !whole ? sum_l : sum_l == 0.f ? 0.f : 1.f / sum_l;
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
+      for (int nb = 0; nb < NB; ++nb) {
+        const float al[2] = {__shfl_sync(0xffffffffu, f, nb * 8 + 2 * t), __shfl_sync(0xffffffffu, f, nb * 8 + 2 * t + 1)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nb][u][e] *= al[e & 1];
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nb][u][e] *= al[e & 1];
+      }
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -824,10 +898,10 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
           const int row_out = row_info[rl].out;
           if (row_out < 0) continue;
           const int gg = (piece & 3) << 1 | piece >> 2;
-          const int at = (d >> 1) * C::kUStride + ((r & 1) + 2 * (d & 1)) * 32 + 4 * gg + (r >> 1);
+          const float* at = merge + (d >> 1) * C::kUStride + ((r & 1) + 2 * (d & 1)) * 32 + 4 * gg + (r >> 1);
           float x = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) x += merge[w * C::kMergeFloats + at];
+          for (int w = 0; w < kWarps; ++w) x += at[w * C::kMergeFloats];
           const int dim = 16 * piece + 2 * u0 + d;
           if (whole) {
             x *= l_all[rl];
@@ -838,21 +912,16 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
               out[row_out + dim] = __half_as_ushort(__float2half_rn(x));
             }
           } else {
-            // place 0: the segment that opens this CTA's range; 1: a later one
-            float* pp = a.partials + ((static_cast<int64_t>(blockIdx.x) * 2 + place) * kByteMaxRows + rl) * kBytePartStride;
+            float* pp = a.partials + (static_cast<int64_t>(place) * kByteMaxRows + rl) * kBytePartStride;
             pp[4 + dim] = x;
-            if (u0 == 0 && i % (8 * kDims) == 0) *reinterpret_cast<float2*>(pp) = make_float2(m_all[rl], l_all[rl]);
+            if (dim == 0) *reinterpret_cast<float2*>(pp) = make_float2(m_all[rl], l_all[rl]);
           }
         }
       }
+    if (!more) break;
     __syncthreads();  // row_info and the sums are the next segment's now
   }
-  if (dead) {
-    if (lane == 0) atomicOr(a.err, kErrTimeout);
-    // copies on their way land (bounded) before the shared memory goes
-    for (int i = 0; i < kRing; ++i)
-      if (pending >> i & 1) bar_wait(bar0 + 8 * i, phases >> i & 1);
-  }
+  if (dead && lane == 0) atomicOr(a.err, kErrTimeout);
 }
 
 // ---- the join ------------------------------------------------------------------
@@ -873,18 +942,15 @@ __device__ __forceinline__ void store2(const ByteAttnArgs& a, uint16_t* p, float
 // The parts of units that more than one CTA attended, joined by their maxima
 // and sums in the order of the CTAs; rows that see nothing become 0.  WARPS
 // warps share a row's parts (1: units are in few parts, and a CTA's 8 warps
-// take 8 rows; 16: a CTA a row).  What depends on the call's inputs alone is
-// worked out before the split pass has to be over.
+// take 8 rows; 16: a CTA a row).
 template <int WARPS>
 __global__ __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) void byte_combine_kernel(const __grid_constant__ ByteAttnArgs a,
-                                                                                      int split_grid, int split_warps,
                                                                                       int rows_per_unit) {
-  constexpr int kThreads = WARPS == 1 ? 256 : 32 * WARPS, kRowsCta = WARPS == 1 ? 8 : 1;
-  __shared__ Sums red[kThreads / 32];
+  constexpr int kRowsCta = WARPS == 1 ? 8 : 1;
   __shared__ float accs[WARPS][128];
   __shared__ float2 ml[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int units = a.layer_count * a.hkv * a.row_blocks, pad = unit_pad(a);
+  const int units = a.layer_count * a.hkv * a.row_blocks;
   int id = blockIdx.x;
   const int row_ctas = rows_per_unit / kRowsCta;
   const int rl = id % row_ctas * kRowsCta + (WARPS == 1 ? warp : 0), slice = WARPS == 1 ? 0 : warp;
@@ -892,39 +958,20 @@ __global__ __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) void byte_combine_ke
   const int u = id % units, b = id / units;
   const Unit un = unit_of(a, u);
   const int row = un.rb * rows_per_unit + rl;
-  const int n = seq_steps(a, b).n;
-  Sums sum{n, n, n > 0}, before{0, 0, 0};
-  if (a.batch > 1) {
-    sum = before;
-    for (int i = tid; i < a.batch; i += kThreads) {
-      const int ni = seq_steps(a, i).n;
-      sum.v += places(ni, pad);
-      sum.r += ni;
-      sum.k += ni > 0;
-      if (i < b) before.v += places(ni, pad);
-    }
-    sum = block_sum<kThreads>(sum, red);
-    before = block_sum<kThreads>(before, red);
-  }
   const int i = row / a.group, hg = row - i * a.group;
   uint16_t* op = static_cast<uint16_t*>(a.out) +
                  (((static_cast<int64_t>(un.li) * a.batch + b) * a.n_q + i) * a.hq + un.h * a.group + hg) * 128 + 4 * lane;
   const bool work = row < a.group * a.n_q;
-  int c0 = 0, parts = 1, first = 0;
-  if (n > 0) {
-    const int64_t s = before.v * units + static_cast<int64_t>(u) * (n + pad);
-    const Shares sh = shares(sum, units, split_grid, split_warps);
-    c0 = sh.of(s + pad);
-    parts = sh.of(s + pad + n - 1) - c0 + 1;
-    // the unit's place in CTA c0: 0 where no step of another unit comes first
-    first = sh.begin(c0) >= s ? 0 : 1;
-  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (n == 0 && work && slice == 0) *reinterpret_cast<uint2*>(op) = make_uint2(0u, 0u);
-  if (n == 0 || parts == 1 || (WARPS > 1 && !work)) return;
+  // where the unit's first part lies, and how many there are
+  const int2 where = __ldcg(a.parts + static_cast<int64_t>(b) * units + u);
+  const int parts = seq_steps(a, b).n == 0 ? 0 : where.y;
+  if (parts == 0 && work && slice == 0) *reinterpret_cast<uint2*>(op) = make_uint2(0u, 0u);
+  if (parts <= 1 || (WARPS > 1 && !work)) return;
   // a warp's parts: slice, slice + WARPS, ..., with the running maximum
-  const float* const part0 = a.partials + (static_cast<int64_t>(c0) * 2 * kByteMaxRows + rl) * kBytePartStride;
+  // (part k > 0 opens its CTA's range)
   constexpr int64_t kPart = 2 * kByteMaxRows * kBytePartStride;
+  const float* const part0 = a.partials + (where.x >> 1) * kPart + rl * kBytePartStride;
   float m = -CUDART_INF_F, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (work) {
@@ -938,7 +985,7 @@ __global__ __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) void byte_combine_ke
         s[j] = make_float2(-CUDART_INF_F, 0.f);
         x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k < parts) {
-          const float* p = part0 + k * kPart + (k == 0 ? first * kByteMaxRows * kBytePartStride : 0);
+          const float* p = part0 + k * kPart + (k == 0 ? (where.x & 1) * kByteMaxRows * kBytePartStride : 0);
           s[j] = __ldcg(reinterpret_cast<const float2*>(p));
           x[j] = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
         }
@@ -997,6 +1044,10 @@ cudaError_t launch_split(const ByteAttnArgs& a, int grid, cudaStream_t stream) {
 
 }  // namespace
 
+size_t byte_parts_bytes(int n_layers, int n_kv_heads, int group, int max_batch, int max_q_tokens) {
+  return static_cast<size_t>(n_layers) * n_kv_heads * ((group * max_q_tokens + 7) / 8) * max_batch * sizeof(int2);
+}
+
 size_t byte_partial_bytes(int n_sms) {
   return static_cast<size_t>(n_sms) * 2 * kByteMaxRows * kBytePartStride * sizeof(float);
 }
@@ -1029,10 +1080,8 @@ cudaError_t launch_byte_attn(const ByteShape& s, ByteAttnArgs& a, cudaStream_t s
   if (e != cudaSuccess) return e;
   // few units: many parts each, a CTA a row; else a warp a row
   if (units * a.batch * 8 <= grid)
-    return launch_dependent(byte_combine_kernel<16>, dim3(static_cast<unsigned>(comb)), dim3(512), 0, stream, a, grid, warps,
-                            8 * nb);
-  return launch_dependent(byte_combine_kernel<1>, dim3(static_cast<unsigned>(comb / 8)), dim3(256), 0, stream, a, grid,
-                          warps, 8 * nb);
+    return launch_dependent(byte_combine_kernel<16>, dim3(static_cast<unsigned>(comb)), dim3(512), 0, stream, a, 8 * nb);
+  return launch_dependent(byte_combine_kernel<1>, dim3(static_cast<unsigned>(comb / 8)), dim3(256), 0, stream, a, 8 * nb);
 }
 
 }  // namespace bgtq

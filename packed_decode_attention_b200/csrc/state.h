@@ -39,6 +39,7 @@ struct bgtq_state {
   bgtq::ByteCacheDev byte_cache;
   CUtensorMap byte_map[2];
   float* byte_partials = nullptr;
+  int2* byte_parts = nullptr;
 };
 
 namespace bgtq {
