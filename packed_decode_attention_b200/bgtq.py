@@ -18,6 +18,7 @@ A decode step, per layer ``l`` (tensors on the GPU; shapes in include/bgtq.h)::
 """
 import ctypes
 import os
+import struct
 from dataclasses import dataclass, fields
 
 import numpy as np
@@ -79,29 +80,18 @@ class _ByteConfig(ctypes.Structure):
     ]
 
 
-class _Score(ctypes.Structure):
-    _fields_ = [
-        ("scale", ctypes.c_double),
-        ("softcap", ctypes.c_double),
-        ("window", ctypes.c_int32),
-        ("reserved", ctypes.c_int32),
-        ("d_slopes", ctypes.c_void_p),
-        ("d_prefix", ctypes.c_void_p),
-        ("d_doc_start", ctypes.c_void_p),
-    ]
+# Structs that a call reads before it returns, packed as C lays them out:
+# bgtq_score (scale, softcap, window, reserved, d_slopes, d_prefix,
+# d_doc_start) and bgtq_rope_config (six int32, axis[64], base).
+_SCORE = struct.Struct("<ddiiQQQ")
+_ROPE = struct.Struct("<6i64sd")
 
 
-class _RopeConfig(ctypes.Structure):
-    _fields_ = [
-        ("n_q_heads", ctypes.c_int32),
-        ("n_kv_heads", ctypes.c_int32),
-        ("head_dim", ctypes.c_int32),
-        ("pairing", ctypes.c_int32),
-        ("dtype", ctypes.c_int32),
-        ("n_axes", ctypes.c_int32),
-        ("axis", ctypes.c_uint8 * N_BLOCKS),
-        ("base", ctypes.c_double),
-    ]
+def _pack(layout, *values):
+    try:
+        return layout.pack(*values)
+    except struct.error as e:
+        raise BgtqError(ERR_INVALID_ARG, str(e))
 
 
 @dataclass
@@ -210,7 +200,7 @@ _SIGS = {
     "bgtq_fork_sequences": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP]),
     "bgtq_resize_sequences": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP]),
     "bgtq_compact_pages": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP]),
-    "bgtq_rope_axes": (ctypes.c_int, [ctypes.POINTER(_RopeConfig), _VP, _I32, _VP, _I32, _VP, _I32, _VP, _I32, _VP, _I32,
+    "bgtq_rope_axes": (ctypes.c_int, [_VP, _VP, _I32, _VP, _I32, _VP, _I32, _VP, _I32, _VP, _I32,
                                       _VP]),
     "bgtq_get_device_error": (ctypes.c_int, [_VP, _VP, _VP]),
     "bgtq_error_string": (ctypes.c_char_p, [_I32]),
@@ -290,10 +280,15 @@ def _refuse(t, name, shape, dtype, device):
 
 
 def _device(device):
-    """torch.device with its index: a state belongs to one GPU."""
+    """torch.device with its index: a state belongs to the GPU that is current when it is made."""
     import torch
     d = torch.device(device)
-    return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+    if d.type != "cuda":
+        return d
+    now = torch.cuda.current_device()
+    if d.index is not None and d.index != now:
+        raise BgtqError(ERR_INVALID_ARG, f"device: {d}, but cuda:{now} is the current one")
+    return torch.device("cuda", now)
 
 
 def _stream(stream):
@@ -482,11 +477,10 @@ def bgtq_byte_append(state, layer, layer_count, d_k, d_v, d_start, d_count, batc
 def bgtq_byte_decode_attn(state, layer, layer_count, d_q, d_seq_lens, batch, n_q, d_out, scale=0.0, softcap=0.0,
                           window=0, d_slopes=None, d_prefix=None, d_doc_start=None, stream=None):
     """The score's fields by keyword (bgtq_score)."""
-    score = at = None
+    score = None
     if scale or softcap or window or d_slopes is not None or d_prefix is not None or d_doc_start is not None:
-        score = _Score(scale, softcap, window, 0, _ptr(d_slopes), _ptr(d_prefix), _ptr(d_doc_start))
-        at = ctypes.addressof(score)
-    _check(lib().bgtq_byte_decode_attn(state, layer, layer_count, _ptr(d_q), _ptr(d_seq_lens), batch, n_q, at,
+        score = _pack(_SCORE, scale, softcap, window, 0, _ptr(d_slopes) or 0, _ptr(d_prefix) or 0, _ptr(d_doc_start) or 0)
+    _check(lib().bgtq_byte_decode_attn(state, layer, layer_count, _ptr(d_q), _ptr(d_seq_lens), batch, n_q, score,
                                        _ptr(d_out), _stream(stream)))
 
 
@@ -528,9 +522,8 @@ def bgtq_rope_axes(n_q_heads, n_kv_heads, pairing, dtype, axis, base, d_q, q_str
         raw = b""
     if len(raw) != N_BLOCKS:
         raise BgtqError(ERR_INVALID_ARG, f"axis: expected {N_BLOCKS} axis numbers")
-    c = _RopeConfig(n_q_heads, n_kv_heads, head_dim, pairing, dtype, n_axes,
-                    (ctypes.c_uint8 * N_BLOCKS).from_buffer_copy(raw), float(base))
-    _check(lib().bgtq_rope_axes(ctypes.byref(c), _ptr(d_q), q_stride, _ptr(d_k), k_stride, _ptr(d_pos), tokens,
+    cfg = _pack(_ROPE, n_q_heads, n_kv_heads, head_dim, pairing, dtype, n_axes, raw, base)
+    _check(lib().bgtq_rope_axes(cfg, _ptr(d_q), q_stride, _ptr(d_k), k_stride, _ptr(d_pos), tokens,
                                 _ptr(d_q_out), q_out_stride, _ptr(d_k_out), k_out_stride, _stream(stream)))
 
 
@@ -557,21 +550,21 @@ def rope_axes(q, k, pos, axis, base, q_out=None, k_out=None, pairing=0):
     one = k if q is None else q
     if not isinstance(one, torch.Tensor) or one.dtype not in (torch.float16, torch.bfloat16) or one.dim() != 3:
         raise BgtqError(ERR_INVALID_ARG, "q, k: one of them is needed, fp16 or bf16 [tokens, heads, 128]")
-    tokens, dev = one.shape[0], one.device
+    tokens, dev, dtype = one.shape[0], one.device, one.dtype
 
     def rows(t, name, heads):
         """(heads, elements from a token to the next)"""
         if t is None:
             return 0, 0
-        if not isinstance(t, torch.Tensor) or t.dtype != one.dtype or t.device != dev or t.dim() != 3:
-            raise BgtqError(ERR_INVALID_ARG, f"{name}: a tensor [tokens, heads, 128] of {one.dtype} on {dev} is expected")
+        if t is not one and (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or t.dim() != 3):
+            raise BgtqError(ERR_INVALID_ARG, f"{name}: a tensor [tokens, heads, 128] of {dtype} on {dev} is expected")
         (n, h, d), (sn, sh, sd) = t.shape, t.stride()
         if n != tokens or d != HEAD_DIM or (heads is not None and h != heads) or n >= 1 << 31:
             raise BgtqError(ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)}, expected "
                                              f"{(tokens, '*' if heads is None else heads, HEAD_DIM)}")
-        if n == 1 or n == 0:
+        if n <= 1:
             sn = h * HEAD_DIM   # there is no next token
-        if sd != 1 or (h > 1 and sh != HEAD_DIM) or sn >= 1 << 31:
+        if sd != 1 or (sh != HEAD_DIM and h > 1) or sn >= 1 << 31:
             raise BgtqError(ERR_INVALID_ARG, f"{name}: strides {t.stride()}, expected contiguous heads")
         return h, sn
 
@@ -583,14 +576,15 @@ def rope_axes(q, k, pos, axis, base, q_out=None, k_out=None, pairing=0):
         k_out = torch.empty((tokens, hkv, HEAD_DIM), dtype=k.dtype, device=dev)
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise BgtqError(ERR_INVALID_ARG, "q_out, k_out: given without q, k")
-    sqo, sko = rows(q_out, "q_out", hq)[1], rows(k_out, "k_out", hkv)[1]
+    sqo = sq if q_out is q else rows(q_out, "q_out", hq)[1]
+    sko = sk if k_out is k else rows(k_out, "k_out", hkv)[1]
     _expect(pos, "pos", (None, tokens), torch.int32, dev)
     if len(axis) != N_BLOCKS:
         raise BgtqError(ERR_INVALID_ARG, f"axis: expected {N_BLOCKS} axis numbers")
-    if dev.type != "cuda" or torch.cuda.current_device() != dev.index:
+    if dev.type != "cuda" or torch._C._cuda_getDevice() != dev.index:
         raise BgtqError(ERR_INVALID_ARG, f"q, k: on {dev}, which is not the current GPU")
     if tokens > 0:
-        bgtq_rope_axes(hq, hkv, pairing, 1 if one.dtype == torch.bfloat16 else 0, axis, base, q, sq, k, sk, pos,
+        bgtq_rope_axes(hq, hkv, pairing, 1 if dtype is torch.bfloat16 else 0, axis, base, q, sq, k, sk, pos,
                        pos.shape[0], tokens, q_out, sqo, k_out, sko)
     return q_out, k_out
 

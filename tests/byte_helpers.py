@@ -45,7 +45,11 @@ def expect(q, k, v, length, n_q, i, rows, score):
     largest score or bias in log2 units).  A score off by d moves its weight by 2 d
     relative, and the sum's by as much; the weights are rounded to fp16
     (2^-11) but the sum is of the rounded ones, so twice that at most; the
-    sums over positions add 2^-20.  Then the output's own rounding."""
+    sums over positions add 2^-20.  Weights are held as 2^14 of the running
+    maximum's, so one far below it is off by half of fp16's least subnormal
+    instead, 2^-25 / 2^14 of the largest weight, and the sum they are divided
+    by is at least the largest: 2^-39 |v_t| a position.  Then the output's
+    own rounding."""
     see = bc.visible(length, n_q, i, score.get("window", 0), score.get("prefix", 0), score.get("doc_start", 0))
     slope, pos = score.get("slope", 0.0), length - n_q + i
     scale = score.get("scale") or 128 ** -0.5
@@ -57,7 +61,7 @@ def expect(q, k, v, length, n_q, i, rows, score):
     cap = score.get("softcap", 0.0)
     top = min(s, cap) if cap else s
     d = s * 2.0 ** -16 + top * 2e-6 + (top + bias) * 2.0 ** -22
-    allowed = mass * (2 * HALF_STEP["fp16"] + 4 * d + 2.0 ** -20)
+    allowed = mass * (2 * HALF_STEP["fp16"] + 4 * d + 2.0 ** -20) + 2.0 ** -39 * np.abs(v[see]).sum(axis=0)
     return want, allowed + HALF_STEP[rows] * (np.abs(want) + allowed) + TINY[rows]
 
 

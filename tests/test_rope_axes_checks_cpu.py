@@ -85,3 +85,17 @@ def test_page_tensors():
     assert status(kv.resize_sequences, t, r, n, i(3), n) == -1 and status(kv.copy_pages, i(2), i(3)) == -1
     assert status(kv.compact_pages, t, r, n, t, r, r2, i(2)) == -1
     assert status(kv.compact_pages, t, r, n, t, r, i(4), i(1)) == -1
+
+
+def test_a_state_is_made_on_the_current_gpu(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert bgtq._device("cuda") == torch.device("cuda", 0) == bgtq._device("cuda:0")
+    assert bgtq._device("cpu") == torch.device("cpu")
+    assert status(bgtq._device, "cuda:1") == -1
+
+
+def test_numbers_that_do_not_fit():
+    assert status(bgtq.bgtq_rope_axes, **{**BASE, "n_q_heads": 1 << 40}) == -1
+    assert status(bgtq.bgtq_rope_axes, **{**BASE, "base": "x"}) == -1
+    for bad in (dict(window=1.5), dict(window=1 << 40), dict(softcap="x")):
+        assert status(bgtq.bgtq_byte_decode_attn, None, 0, 1, 16, 16, 1, 1, 16, **bad) == -1
