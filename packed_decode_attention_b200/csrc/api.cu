@@ -346,7 +346,7 @@ int bgtq_create(const bgtq_config* cfg, void* d_cache, size_t cache_bytes, void*
   if ((reinterpret_cast<uintptr_t>(d_cache) | reinterpret_cast<uintptr_t>(d_workspace)) % kAlign) return BGTQ_ERR_ALIGNMENT;
   const Layout p = plan(cfg);
   if (cache_bytes < p.cache_total || workspace_bytes < p.ws_total) return BGTQ_ERR_BUFFER_SIZE;
-  if (cfg->page_pool_tiles > 0 && bgtq::page_copy_setup() != cudaSuccess) return BGTQ_ERR_CUDA;
+  if (cfg->page_pool_tiles > 0 && bgtq::page_setup() != cudaSuccess) return BGTQ_ERR_CUDA;
   bgtq_state* st = new (std::nothrow) bgtq_state();
   if (!st) return BGTQ_ERR_HOST_ALLOC;
   st->cfg = *cfg;

@@ -141,7 +141,7 @@ int bgtq_byte_create(const bgtq_byte_config* cfg, void* d_cache, size_t cache_by
   if (cudaGetDevice(&dev) != cudaSuccess) return BGTQ_ERR_CUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return BGTQ_ERR_CUDA;
   if (bgtq::byte_decode_setup() != cudaSuccess) return BGTQ_ERR_CUDA;
-  if (cfg->page_pool_tiles > 0 && bgtq::page_copy_setup() != cudaSuccess) return BGTQ_ERR_CUDA;
+  if (cfg->page_pool_tiles > 0 && bgtq::page_setup() != cudaSuccess) return BGTQ_ERR_CUDA;
   bgtq_state* st = new (std::nothrow) bgtq_state();
   if (!st) return BGTQ_ERR_HOST_ALLOC;
   st->byte = true;

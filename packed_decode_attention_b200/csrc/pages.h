@@ -66,8 +66,8 @@ struct PagePlanArgs {
   int32_t n_pages, batch;
 };
 
-// Sets the copy kernel's shared-memory limit on the current device.
-cudaError_t page_copy_setup();
+// Sets the kernels' shared-memory limits on the current device.
+cudaError_t page_setup();
 // Copies pages src[i] to dst[i], i < n_pairs (n_pairs_dev null) or, after the
 // plan that the stream holds, i < *n_pairs_dev <= n_pairs.
 cudaError_t launch_page_copy(const PageArrays& c, const int32_t* src, const int32_t* dst, int n_pairs,

@@ -137,6 +137,14 @@ def test_fork_matches_oracle(dev, kind, seed):
     check_fork(kv, dev, parent, table, refs, lens, in_place=seed % 2 == 1)
 
 
+def test_fork_of_more_rows_than_one_cta_plans(dev):
+    rng = random.Random(11)
+    batch, width, pool = 257, 3, 900
+    table, refs, lens = state(rng, batch, width, pool)
+    parent = [rng.choice([b, 0, rng.randint(-1, batch - 1)]) for b in range(batch)]
+    check_fork(cache("int8", dev, batch, 64 * width, pool, layers=1), dev, parent, table, refs, lens)
+
+
 @pytest.mark.parametrize("case", ["stay", "all_of_one", "free_all", "rotate"])
 def test_fork_patterns(dev, case):
     batch, width, pool = 9, 5, 70
@@ -217,6 +225,29 @@ def test_resize_matches_oracle(dev, kind, seed):
     table, refs, lens = check_resize(kv, dev, rows, refs, lens, new, ["other", "lens", "new"][seed % 3])
     new = [rng.choice([n, min(64 * width, n + 1), rng.randint(n, 64 * width), 64 * width]) for n in lens]
     check_resize(kv, dev, table, refs, lens, new, ["new", "other", "lens"][seed % 3])
+
+
+def test_resize_and_compact_of_a_large_pool(dev):
+    """A pool past what one CTA's shared memory plans."""
+    rng = random.Random(9)
+    batch, width, pool = 300, 70, 17000
+    kv = cache("int8", dev, batch, 64 * width, pool, layers=1, hkv=1)
+    table, refs, lens = state(rng, batch, width, pool, other=300)
+    parent = [rng.choice([b, rng.randint(-1, batch - 1)]) for b in range(batch)]
+    table, refs, lens = check_fork(kv, dev, parent, table, refs, lens)
+    table = [r[:pages.held(n)] + [-1] * (width - pages.held(n)) for r, n in zip(table, lens)]
+    new = [rng.choice([0, n, n // 2, min(64 * width, n + 70)]) for n in lens]
+    table, refs, lens = check_resize(kv, dev, table, refs, lens, new)
+    rows, r, to, n, pairs = pages.compact(table, refs, lens)
+    want = moved(slots(kv), pairs)
+    tb, rf = i32(table, dev), i32(refs, dev)
+    mp, live = torch.empty_like(rf), i32([0], dev)
+    kv.compact_pages(tb, rf, i32(lens, dev), tb, rf, mp, live)
+    assert live.item() == n and mp.tolist() == to and rf.tolist() == r and tb.tolist() == rows
+    assert same_bytes(kv, want) and kv.device_error() == 0
+    # and where the pool runs out
+    new = [64 * width] * batch
+    check_resize(kv, dev, rows, r, lens, new)
 
 
 def test_resize_with_too_few_pages(dev):
