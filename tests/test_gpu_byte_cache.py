@@ -111,6 +111,15 @@ def test_append_paged_and_capacity(dev, code):
     assert np.array_equal(got[22:], np.zeros((42, 128)))    # behind the capacity: as it was
 
 
+def test_append_of_no_rows_touches_nothing(dev):
+    """No rows, or none within the capacity, in the middle of a block that nothing was written to."""
+    kv = bgtq.ByteKVCache(bgtq.ByteConfig(1, 2, 2, 3, 100), dev)
+    before = kv.cache.clone()
+    k = torch.ones((1, 3, 4, 2, 128), dtype=torch.float16, device=dev)
+    kv.append(0, k, k, i32([70, 120, 2 ** 31 - 2], dev), i32([0, 3, 4], dev))
+    assert torch.equal(kv.cache, before) and kv.device_error() == bgtq.DEVERR_CAPACITY
+
+
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("rt", ROWS)
 def test_append_special_values(dev, code, rt):
