@@ -38,8 +38,7 @@ __device__ __forceinline__ uint32_t narrow2(float x, float y) {
 // 2 l and 2 l + 1 once for all heads; lane (h, c) = (l / 8, l % 8) turns
 // blocks 8 c .. 8 c + 7 of head h, 16 bytes of each half of the row (pairing
 // 0) or 32 in a row (pairing 1).  Bound by HBM: 32768 tokens of 40 heads take
-// 107.6 us, 95 % of the copy rate (with the sines computed for every row it
-// would be bound by them; a warp a token computes them once).
+// 107.6 us, 95 % of the copy rate.
 template <bool BF16>
 __global__ __launch_bounds__(32 * kRopeWarps) void rope_axes_kernel(const __grid_constant__ RopeAxesArgs a) {
   const int lane = threadIdx.x & 31, h = lane >> 3, c = lane & 7;
