@@ -157,6 +157,7 @@ class ByteConfig:
 
 
 _lib = None
+_compiled = None
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _SIGS = {
@@ -220,6 +221,17 @@ def lib():
             fn.argtypes = args
         _lib = handle
     return _lib
+
+
+def marshal():
+    """The checks and calls of the serving operators as compiled code (raises
+    if it has not been built; loads libbgtq.so)."""
+    global _compiled
+    if _compiled is None:
+        lib()
+        from . import _marshal
+        _compiled = _marshal
+    return _compiled
 
 
 def declared_symbols():
@@ -547,6 +559,12 @@ def rope_axes(q, k, pos, axis, base, q_out=None, k_out=None, pairing=0):
     Returns (q_out, k_out).
     """
     import torch
+    if (q is None) == (q_out is None) and (k is None) == (k_out is None):
+        status = marshal().rope_axes(torch.float16, torch.bfloat16, torch.int32, q, k, pos, axis, base, q_out, k_out,
+                                     pairing)
+        if status is not None:
+            _check(status)
+            return q_out, k_out
     one = k if q is None else q
     if not isinstance(one, torch.Tensor) or one.dtype not in (torch.float16, torch.bfloat16) or one.dim() != 3:
         raise BgtqError(ERR_INVALID_ARG, "q, k: one of them is needed, fp16 or bf16 [tokens, heads, 128]")
@@ -595,11 +613,25 @@ class _Pages:
     all on the device)."""
 
     page_scratch = None
+    # what the compiled checks compare tensors with; a call whose arguments they
+    # do not pass goes through the checks here, which say what is wrong
+    _ctx = None
 
-    def _make_page_scratch(self):
+    def _make_context(self, rows):
         import torch
-        if self.cfg.page_pool_tiles > 0:
+        c = self.cfg
+        if c.page_pool_tiles > 0:
             self.page_scratch = torch.empty(bgtq_page_scratch_bytes(self.state), dtype=torch.uint8, device=self.device)
+        self._fast = marshal()
+        self._ctx = self._fast.context(self.device, self.device.index, rows, torch.int32, torch.float32, c.n_kv_heads,
+                                       c.n_q_heads, (c.capacity_tokens + TILE - 1) // TILE, c.page_pool_tiles,
+                                       0 if self.page_scratch is None else self.page_scratch.data_ptr())
+
+    def _through(self, status):
+        """Whether a compiled call was made (None: it was not); its error, if any, is raised."""
+        if status:
+            _check(status)
+        return status is not None
 
     def _page_args(self, batch, tables=(), refs=(), per_row=()):
         import torch
@@ -613,6 +645,8 @@ class _Pages:
 
     def copy_pages(self, src, dst):
         """Page src[i] to dst[i] (int32 [n]); no page twice in dst or in both lists."""
+        if self._ctx is not None and self._through(self._fast.copy_pages(self._ctx, self.state, src, dst)):
+            return
         import torch
         _expect(src, "src", (None,), torch.int32, self.device)
         _expect(dst, "dst", tuple(src.shape), torch.int32, self.device)
@@ -622,6 +656,9 @@ class _Pages:
     def fork_sequences(self, parent, table, refs, lens, table_out, refs_out, lens_out):
         """Row b becomes a fork of row parent[b] (-1: empty): whole pages shared, partly filled ones copied for
         every holder but one.  refs_out may be refs, lens_out lens; table_out is another table."""
+        if self._ctx is not None and self._through(self._fast.fork_sequences(
+                self._ctx, self.state, parent, table, refs, lens, table_out, refs_out, lens_out)):
+            return
         import torch
         _expect(parent, "parent", (None,), torch.int32, self.device)
         batch = parent.shape[0]
@@ -634,6 +671,9 @@ class _Pages:
         """Row b from lens[b] to new_lens[b] positions: pages given back (0: all) or taken, a shared last page copied
         before it is written.  table and refs change in place; lens_out: the lengths granted (may be lens or
         new_lens)."""
+        if self._ctx is not None and self._through(self._fast.resize_sequences(
+                self._ctx, self.state, table, refs, lens, new_lens, lens_out)):
+            return
         import torch
         _expect(lens, "lens", (None,), torch.int32, self.device)
         batch = lens.shape[0]
@@ -643,6 +683,9 @@ class _Pages:
     def compact_pages(self, table, refs, lens, table_out, refs_out, page_map, n_live):
         """Live pages (refs > 0) move to ids 0 .. n_live - 1.  page_map int32 [pages]: new ids, -1 for free ones;
         n_live int32 [1].  table_out may be table, refs_out refs."""
+        if self._ctx is not None and self._through(self._fast.compact_pages(
+                self._ctx, self.state, table, refs, lens, table_out, refs_out, page_map, n_live)):
+            return
         import torch
         _expect(lens, "lens", (None,), torch.int32, self.device)
         _expect(n_live, "n_live", (1,), torch.int32, self.device)
@@ -665,7 +708,7 @@ class PackedKVCache(_Pages):
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         self.state = bgtq_create(cfg, self.cache, self.cache_bytes, self.workspace, self.workspace_bytes)
         self.offsets = bgtq_cache_offsets(self.state)
-        self._make_page_scratch()
+        self._make_context(torch.float16)
 
     def close(self):
         if getattr(self, "state", None):
@@ -906,7 +949,7 @@ class ByteKVCache(_Pages):
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         self.state = bgtq_byte_create(cfg, self.cache, self.cache_bytes, self.workspace, self.workspace_bytes)
         self.offsets = bgtq_cache_offsets(self.state)
-        self._make_page_scratch()
+        self._make_context(self.row_dtype)
 
     def close(self):
         if getattr(self, "state", None):
@@ -961,6 +1004,9 @@ class ByteKVCache(_Pages):
     # -- calls (tensors checked as PackedKVCache checks its own) --
     def append(self, layer, k, v, start, count, layer_count=1):
         """k, v [layer_count, batch, n, Hkv, 128] of the cache's row type; start, count int32 [batch]."""
+        if self._ctx is not None and self._through(self._fast.append(
+                self._ctx, self.state, layer, layer_count, k, v, start, count)):
+            return
         import torch
         _expect(k, "k", (layer_count, None, None, self.cfg.n_kv_heads, HEAD_DIM), self.row_dtype, self.device)
         _expect(v, "v", tuple(k.shape), self.row_dtype, self.device)
@@ -980,6 +1026,10 @@ class ByteKVCache(_Pages):
         every query.  doc_start int32 [batch, n_q]: the first position of each
         query's document.
         """
+        if self._ctx is not None and self._through(self._fast.decode_attn(
+                self._ctx, self.state, layer, layer_count, q, seq_lens, out, scale, softcap, slopes, window, prefix,
+                doc_start)):
+            return
         import torch
         dt = self.row_dtype
         _expect(q, "q", (layer_count, None, None, self.cfg.n_q_heads, HEAD_DIM), dt, self.device)

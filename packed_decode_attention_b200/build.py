@@ -1,11 +1,14 @@
-"""Builds the in-tree shared library libbgtq.so for sm_100a with nvcc."""
+"""Builds the in-tree shared library libbgtq.so for sm_100a with nvcc, and _marshal.so (the Python binding's checks and
+calls of the serving operators), which links to it."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libbgtq.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 SOURCES = ["csrc/encode.cu", "csrc/decode.cu", "csrc/diag.cu", "csrc/api.cu", "csrc/host_tables.cpp",
            "csrc/byte_append.cu", "csrc/byte_decode.cu", "csrc/api_byte.cu", "csrc/pages.cu", "csrc/api_pages.cu",
            "csrc/rope.cu", "csrc/api_rope.cu"]
@@ -31,14 +34,26 @@ def up_to_date():
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
-def build(force=False, verbose=False):
-    if not force and up_to_date():
-        return LIB
-    nvcc = os.environ.get("NVCC", "nvcc")
-    cmd = [nvcc] + NVCC_FLAGS + ["-o", LIB] + [os.path.join(PKG, s) for s in SOURCES]
+def build_marshal(force=False, verbose=False):
+    src, header = os.path.join(PKG, "csrc", "marshal.c"), os.path.join(ROOT, "include", "bgtq.h")
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= max(map(os.path.getmtime, (src, header))):
+        return MARSHAL
+    cmd = [os.environ.get("CC", "gcc"), "-shared", "-fPIC", "-O2", "-std=c11", "-Wall", "-I",
+           sysconfig.get_paths()["include"], "-o", MARSHAL, src, "-L", PKG, "-lbgtq", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
+    return MARSHAL
+
+
+def build(force=False, verbose=False):
+    if force or not up_to_date():
+        nvcc = os.environ.get("NVCC", "nvcc")
+        cmd = [nvcc] + NVCC_FLAGS + ["-o", LIB] + [os.path.join(PKG, s) for s in SOURCES]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+    build_marshal(force, verbose)
     return LIB
 
 
