@@ -459,8 +459,7 @@ int bgtq_get_decode_path(bgtq_state* st, int32_t* h_fused, int32_t* h_ctas);
  * allocation comes before it.  A state made by bgtq_byte_create works with
  * bgtq_destroy, bgtq_cache_offsets, bgtq_set_block_table,
  * bgtq_test_drop_tile_copies, bgtq_get_device_error, the page operations and
- * the calls below; the
- * packed cache's other calls answer BGTQ_ERR_NOT_READY or
+ * the calls below; the packed cache's other calls answer BGTQ_ERR_NOT_READY or
  * BGTQ_ERR_INVALID_ARG for it, and the bgtq_byte_* calls
  * BGTQ_ERR_INVALID_ARG for a packed state.
  *
@@ -470,7 +469,8 @@ int bgtq_get_decode_path(bgtq_state* st, int32_t* h_fused, int32_t* h_ctas);
  *                                   = position 64 t + p, plain order
  *   scales  fp32 [slots]            a power of two, at least 2^-100
  * The value of a code is code * scale.  One scale for the 64 positions of a
- * (layer, sequence or page, KV head) block, K and V apart. */
+ * (layer, sequence or page, KV head) block, K and V apart.  Device pointers of
+ * the bgtq_byte_* calls are 16-byte aligned. */
 enum { BGTQ_CODE_E4M3 = 0, BGTQ_CODE_INT = 1 };       /* int: int8, -127 .. 127 */
 enum { BGTQ_DTYPE_HALF = 0, BGTQ_DTYPE_BFLOAT = 1 };  /* fp16, bf16 */
 

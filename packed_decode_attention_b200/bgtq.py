@@ -610,7 +610,8 @@ def rope_axes(q, k, pos, axis, base, q_out=None, k_out=None, pairing=0):
 class _Pages:
     """The page operations of a paged cache (include/bgtq.h: rows' block table
     int32 [batch, ceil(capacity / 64)], refs int32 [pages], lens int32 [batch],
-    all on the device)."""
+    all on the device).  The calls of one cache share a scratch buffer: issue
+    them on one stream, or order the streams."""
 
     page_scratch = None
     # what the compiled checks compare tensors with; a call whose arguments they
