@@ -318,17 +318,18 @@ __device__ __forceinline__ void start_of(int64_t off, int64_t left, int pad, Cur
   total = static_cast<int>(left - static_cast<int64_t>(seg.u) * seg.s.n - seg.j);
 }
 
-// NB blocks of 8 query rows.  One: 12 warps of 168 registers, two pairs of
-// buffers each (a step's K and V); two, with twice the accumulators: 8 warps
-// of 255, three pairs.  More than 16 rows take several passes.  (16 warps of 128
-// registers spill: the ragged batch 99 us; 8 of 221 in steps of 64 positions,
-// as many bytes on their way, 86; 12 are 82.)  Either keeps 192 KB a SM on
-// their way, where 64 reach the read rate.
+// NB blocks of 8 query rows.  One: 12 warps of 168 registers; two, with twice
+// the accumulators: 8 warps of 255 (12 of 168 spill: 39 us where these take 28).
+// More than 16 rows take several passes.  (One block, the ragged batch: 16
+// warps of 128 registers spill, 99 us; 8 of 221 in steps of 64 positions, 86; 12
+// are 82.)  Two pairs of buffers a warp (a step's K and V) keep 192 or 128 KB an
+// SM on their way, where 64 reach the read rate (three pairs for two blocks
+// were 5 % slower).
 template <int NB>
 struct Split {
   static constexpr int kWarps = NB == 1 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kRing = NB == 1 ? 2 : 3;         // pairs of buffers
+  static constexpr int kRing = 2;                         // pairs of buffers
   static constexpr int kRows = 8 * NB;
   static constexpr int kQPitch = 136;                   // halves: rows 4 banks apart
   static constexpr int kUStride = 129;                  // merge: floats from a dimension pair to the next
