@@ -1,8 +1,10 @@
 """Python binding of the C ABI in include/bgtq.h (ctypes, argument marshalling only).
 
 Every ``bgtq_*`` function here calls the function of the same name in the
-in-tree ``libbgtq.so``; nothing is computed in Python.  ``PackedKVCache``
-owns the two device buffers (torch tensors) and one library state.
+in-tree ``libbgtq.so``; nothing is computed in Python.  ``PackedKVCache`` and
+``ByteKVCache`` (8-bit codes) own the two device buffers (torch tensors) and
+one library state; ``rope_axes`` needs none.  The serving operators' methods
+go through compiled checks (``_marshal.so``) where their arguments are in order.
 
 The library must be built (``python -m packed_decode_attention_b200.build``
 or ``__graft_entry__.build()``); importing the binding without it raises.
@@ -229,7 +231,10 @@ def marshal():
     global _compiled
     if _compiled is None:
         lib()
-        from . import _marshal
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is missing: build it with `python -m packed_decode_attention_b200.build`") from e
         _compiled = _marshal
     return _compiled
 
