@@ -45,6 +45,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// What is added to a score before ex2: kPShift - m for the running maximum m
+// (0 where nothing was seen: the scores are -inf).  From 2^24 on the sum does
+// not hold kPShift exactly; rounded down, the largest weight stays at most
+// 2^14, where to nearest it would be 2^16 and more, past fp16.
+__device__ __forceinline__ float weight_shift(float m) {
+  if (m == -CUDART_INF_F) return 0.f;
+  return fabsf(m) < 16777216.f ? kPShift - m : __fadd_rd(kPShift, -m);
+}
+
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
   for (int i = 0; i < kByteWaitLimit; ++i) {
     uint32_t ok;
@@ -772,8 +781,7 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
           // weights 2^14 2^(x - m) in fp16: the tensor cores' type, rounded
           // once (2^-11 relative); the factor keeps weights down to 2^-28 of
           // the largest out of fp16's subnormals, and cancels in acc / l
-          const float s0 = m[nb][0] == -CUDART_INF_F ? 0.f : kPShift - m[nb][0];
-          const float s1 = m[nb][1] == -CUDART_INF_F ? 0.f : kPShift - m[nb][1];
+          const float s0 = weight_shift(m[nb][0]), s1 = weight_shift(m[nb][1]);
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
