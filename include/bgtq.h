@@ -547,6 +547,9 @@ typedef struct {
  *   d_seq_lens   int32 [batch], 0..capacity, the new tokens counted
  *   n_q          1..max_q_tokens
  *   score        host memory, read before the call returns; NULL: the defaults
+ * Positions that no query of the call sees may hold anything (codes and
+ * scales of a buffer never written); the others hold what an append stored,
+ * which is never a NaN code.
  * Scores, softmax statistics and sums are fp32; the softmax weights are
  * rounded to fp16 before they meet the (exact) codes.  A query that sees
  * nothing gives 0 (so do queries before position 0, where n_q >

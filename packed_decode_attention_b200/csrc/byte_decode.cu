@@ -23,6 +23,8 @@
 // cycles of an SM quarter each, 32 for 32 positions, where HBM gives 360 cycles).
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "byte_cache.h"
 #include "common.cuh"
 
@@ -592,7 +594,7 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
 
   while (f0 < mine_total) {
     const int len_seg = min(seg.s.n - seg.j, mine_total - f0);
-    const int len = seg.s.len, pre = seg.s.pre;
+    const int pre = seg.s.pre;
 
     // q as the products' 8-column operand, scaled by a power of two a row so
     // that its largest element lies in [2^14, 2^15): fp16 and bf16 queries
@@ -705,6 +707,7 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
           }
         }
         uint32_t pf[NB][2][2];
+        uint32_t seen = 0;     // bit i: some row sees position 8 i + pig of a step that is not full
         const bool full = (p0 >= lo_max && p0 + kStep - 1 <= hi_min) || p0 + kStep <= pre;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -749,8 +752,27 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
 #pragma unroll
                 for (int e = c; e < 4; e += 2) {
                   const int p = p0 + 16 * mt + 8 * (e >> 1) + pig;
-                  if (!(p < r.pre || (p >= r.lo && p <= r.hi))) S[nb][mt][e] = -CUDART_INF_F;
+                  if (p < r.pre || (p >= r.lo && p <= r.hi))
+                    seen |= 1u << (2 * mt + (e >> 1));
+                  else
+                    S[nb][mt][e] = -CUDART_INF_F;
                 }
+            }
+            // positions that no row sees (behind the sequence, before a
+            // document or the window) may never have been written, and a NaN
+            // code times a zero weight is NaN: their V rows are cleared
+            if (CODE == 0 && nb == NB - 1) {
+              seen |= __shfl_xor_sync(0xffffffffu, seen, 1);
+              seen |= __shfl_xor_sync(0xffffffffu, seen, 2);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!(seen >> i & 1)) {
+                  const uint32_t at = vb + (8 * i + pig) * 128 + t * 32;
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16), "r"(0) : "memory");
+                }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
             }
           }
           float mx[2] = {m[nb][0], m[nb][1]};
@@ -794,14 +816,8 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
               l[nb][1] += f.y;
             }
         }
-        if (CODE == 0 && p0 + kStep > len) {
-          // positions behind the sequence may hold anything, and a NaN code
-          // times a zero weight is NaN
-          for (int p = len - p0; p < kStep; ++p)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vb + p * 128 + lane * 4), "r"(0) : "memory");
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
+        // a block that no row sees any of may have any scale, and 0 times it is to be 0
+        vs[0] = fminf(fmaxf(vs[0], 0.f), FLT_MAX);
         // 4 of the 8 M-tiles (dimension pairs) at a time: half of each 16-byte piece
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
