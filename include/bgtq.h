@@ -531,7 +531,7 @@ int bgtq_byte_append(bgtq_state* st, int32_t layer, int32_t layer_count, const v
  * of the call's queries, before and behind their own position, whatever the
  * window and the document (attention sinks, a prompt attended both ways). */
 typedef struct {
-  double scale;                /* 0: 1/sqrt(128); else finite, 0 < scale <= 1e30 */
+  double scale;                /* 0: 1/sqrt(128); else 0 < scale <= 16384 */
   double softcap;              /* 0: none; else 1e-30..1e30 */
   int32_t window;              /* 0: none; else a query sees its own position and the window - 1 before it */
   int32_t reserved;            /* not read */
@@ -550,7 +550,9 @@ typedef struct {
  * Positions that no query of the call sees may hold anything (codes and
  * scales of a buffer never written); the others hold what an append stored,
  * which is never a NaN code.
- * Scores, softmax statistics and sums are fp32; the softmax weights are
+ * Scores, softmax statistics and sums are fp32 (scale q . k past 2^57, which
+ * only bf16 rows reach, may count as less than it is, but past 2^57; a
+ * slope past 2^95 counts as 2^95); the softmax weights are
  * rounded to fp16 before they meet the (exact) codes.  A query that sees
  * nothing gives 0 (so do queries before position 0, where n_q >
  * seq_lens[b]).  A length out of range sets BGTQ_DEVERR_SEQ_LEN and counts

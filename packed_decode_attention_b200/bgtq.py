@@ -1025,8 +1025,8 @@ class ByteKVCache(_Pages):
         """Attention of the last n_q tokens of each sequence.
 
         q, out: [layer_count, batch, n_q, Hq, 128] of the cache's row type; seq_lens
-        int32 [batch], the new tokens counted.  scale: of q . k (None:
-        1/sqrt(128)).  softcap c: scores become c tanh(x / c).  slopes fp32
+        int32 [batch], the new tokens counted.  scale: of q . k (up to 16384;
+        None: 1/sqrt(128)).  softcap c: scores become c tanh(x / c).  slopes fp32
         [Hq]: slope * distance is taken off.  window: positions a query sees,
         its own included.  prefix int32 [batch]: positions below it are seen by
         every query.  doc_start int32 [batch, n_q]: the first position of each

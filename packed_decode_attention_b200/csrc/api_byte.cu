@@ -226,7 +226,7 @@ int bgtq_byte_decode_attn(bgtq_state* st, int32_t layer, int32_t layer_count, co
   double scale = 0.0;
   if (score) {
     scale = score->scale;
-    if (!std::isfinite(scale) || scale < 0.0 || scale > 1e30) return BGTQ_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || scale < 0.0 || scale > 16384.0) return BGTQ_ERR_INVALID_ARG;
     if (!std::isfinite(score->softcap) || score->softcap < 0.0 || score->softcap > 1e30) return BGTQ_ERR_INVALID_ARG;
     if (score->window < 0) return BGTQ_ERR_INVALID_ARG;
     if (!aligned16(score->d_slopes) || !aligned16(score->d_prefix) || !aligned16(score->d_doc_start))

@@ -56,6 +56,15 @@ __device__ __forceinline__ float weight_shift(float m) {
   return fabsf(m) < 16777216.f ? kPShift - m : __fadd_rd(kPShift, -m);
 }
 
+// Products q . codes stay under 2^31 (128 of 2^15 by 448).  Their factor is cut
+// to kMaxFactor and slopes to kMaxSlope (distances are at most 2^30), so that a
+// score, in log2 units and with its bias, stays in fp32.  A product that is not
+// 0 is at least 2^-33 (fp16's least times e4m3's), so what is cut is a score
+// past 2^57, and it stays one: a softmax that steep takes its largest score
+// whichever way.  (Cutting the scores themselves: 5 % slower for short sequences.)
+constexpr float kMaxFactor = 0x1p90f;
+constexpr float kMaxSlope = 0x1p96f;
+
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
   for (int i = 0; i < kByteWaitLimit; ++i) {
     uint32_t ok;
@@ -352,7 +361,7 @@ struct Split {
 };
 
 struct Row {
-  float back;     // undoes the query's scaling, times the scores' scale
+  float back;     // undoes the query's scaling, times the scores' scale (at most 2^113 2^14)
   float slope;    // in log2 units
   int32_t lo, hi; // sees lo .. hi
   int32_t pre;    // and positions below
@@ -628,7 +637,7 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
           r.lo = asked.lo;
           r.hi = asked.p;
           r.pre = pre;
-          r.slope = asked.slope * kLog2e;
+          r.slope = fminf(fmaxf(asked.slope * kLog2e, -kMaxSlope), kMaxSlope);
           // distances count from the row's last visible position: its
           // weights do not change, and the near ones stay exact
           r.tref = max(asked.lo <= asked.p ? asked.p : -1, pre - 1);
@@ -712,7 +721,7 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           // scores in log2 units
-          const float f0c = colf[nb][0] * ks[0], f1c = colf[nb][1] * ks[0];
+          const float f0c = fminf(colf[nb][0] * ks[0], kMaxFactor), f1c = fminf(colf[nb][1] * ks[0], kMaxFactor);
           if (a.cap > 0.f) {
             const float ic = 1.f / a.cap, oc = a.cap * kLog2e;
 #pragma unroll

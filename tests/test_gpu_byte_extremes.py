@@ -1,7 +1,9 @@
-"""Attention over the 8-bit cache at the ends of its ranges: scores of any size."""
+"""Attention over the 8-bit cache at the ends of its ranges: scores, scales and biases of any size."""
 import numpy as np
 import pytest
 import torch
+
+from packed_decode_attention_b200 import bgtq
 
 from byte_helpers import HALF_STEP, TINY, make, values
 
@@ -15,6 +17,10 @@ def dev():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     return torch.device("cuda:0")
+
+
+def i32(v, dev):
+    return torch.tensor(v, dtype=torch.int32, device=dev)
 
 
 def close(got, want, mass, rows):
@@ -38,3 +44,51 @@ def test_scores_of_every_size(dev, code):
         for r in range(4):
             assert close(out[0, 0, 0, r], v[0, 0], np.abs(v[0, 0]), "bf16"), (e, r)
             assert close(out[0, 1, 0, r], v[1, :2].mean(0), np.abs(v[1, :2]).mean(0), "bf16"), (e, r)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+def test_scores_past_fp32(dev, softcap):
+    """Scores that fp32 does not hold: the largest one wins, and zero codes under a huge scale score 0."""
+    kv, q, out, sl, _ = make(dev, [5, 1], hkv=1, group=4, code="int8", rows="bf16")
+    k = kv.k_codes()
+    k.zero_()
+    k[0, 0, 0, 0, 2, 0], k[0, 0, 0, 0, 4, 0], k[0, 0, 0, 0, 3, 1], k[0, 1, 0, 0, 0, :2] = 1, -1, -1, -1
+    kv.k_scales().fill_(2.0 ** 100)
+    q.zero_()
+    q[..., 0, 0], q[..., 1, 0], q[..., 2, 1] = 2.0 ** 120, -2.0 ** 120, 2.0 ** 120
+    kv.decode_attn(0, q, sl, out, softcap=softcap)
+    v = values(kv.v_codes(), kv.v_scales())[0, :, 0, 0]
+    sign = np.array([[0, 0, 1, 0, -1], [0, 0, -1, 0, 1], [0, 0, 0, -1, 0], [0, 0, 0, 0, 0]])
+    for r in range(4):
+        x = sign[r] * (softcap or 1e30)
+        w = np.exp(x - x.max())
+        w /= w.sum()
+        # capped scores: tanh's 1e-6 of 5, twice in a weight and its sum; weights in fp16 (2^-11, twice)
+        extra = (4e-5 + 2.0 ** -10) * (w @ np.abs(v[0, :5])) if softcap else 0.0
+        got = out[0, 0, 0, r].double().cpu().numpy()
+        want = w @ v[0, :5]
+        allowed = extra + (2.0 ** -10 + 2.0 ** -19) * (w @ np.abs(v[0, :5]))   # the mean of 4 or 5: equal weights
+        assert np.all(np.abs(got - want) <= allowed + HALF_STEP["bf16"] * (np.abs(want) + allowed)), r
+        assert close(out[0, 1, 0, r], v[1, 0], np.abs(v[1, 0]), "bf16"), r
+
+
+def test_scale_bounds(dev):
+    kv, q, out, sl, _ = make(dev, [70], hkv=1, group=4, rows="bf16")
+    kv.decode_attn(0, q, sl, out, scale=16384.0)
+    assert torch.isfinite(out).all()
+    for bad in (16385.0, 1e30, float("inf"), float("nan"), -1.0):
+        with pytest.raises(bgtq.BgtqError) as e:
+            kv.decode_attn(0, q, sl, out, scale=bad)
+        assert e.value.status == -1
+
+
+@pytest.mark.parametrize("rt", ["fp16", "bf16"])
+def test_slopes_of_the_largest_size(dev, rt):
+    """A bias so steep that one position is left: the nearest, or the farthest where the slope is negative."""
+    kv, q, out, sl, _ = make(dev, [700], hkv=1, group=4, code="int8", rows=rt)
+    big = torch.finfo(torch.float32).max
+    kv.decode_attn(0, q, sl, out, slopes=torch.tensor([big, 1e30, -big, -1e30], device=dev), prefix=i32([5], dev),
+                   window=100)
+    v = values(kv.v_codes(), kv.v_scales())[0, 0, 0].reshape(-1, 128)
+    for r, at in enumerate((699, 699, 0, 0)):
+        assert close(out[0, 0, 0, r], v[at], np.abs(v[at]), rt), r
