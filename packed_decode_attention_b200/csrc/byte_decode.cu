@@ -48,12 +48,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // What is added to a score before ex2: kPShift - m for the running maximum m
-// (0 where nothing was seen: the scores are -inf).  From 2^24 on the sum does
-// not hold kPShift exactly; rounded down, the largest weight stays at most
-// 2^14, where to nearest it would be 2^16 and more, past fp16.
+// (0 where nothing was seen: the scores are -inf), rounded down, so that the
+// largest weight is at most 2^14.  To nearest it would be 2^16 and more, past
+// fp16, for m of 2^25 to 2^28, where fp32 does not hold kPShift - m.
 __device__ __forceinline__ float weight_shift(float m) {
-  if (m == -CUDART_INF_F) return 0.f;
-  return fabsf(m) < 16777216.f ? kPShift - m : __fadd_rd(kPShift, -m);
+  return m == -CUDART_INF_F ? 0.f : __fadd_rd(kPShift, -m);
 }
 
 // Products q . codes stay under 2^31 (128 of 2^15 by 448).  Their factor is cut
