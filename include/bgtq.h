@@ -552,8 +552,9 @@ typedef struct {
  * which is never a NaN code.
  * Scores, softmax statistics and sums are fp32 (scale q . k past 2^57, which
  * only bf16 rows reach, may count as less than it is, but past 2^57; a
- * slope past 2^95 counts as 2^95); the softmax weights are
- * rounded to fp16 before they meet the (exact) codes.  A query that sees
+ * slope past 2^95 counts as 2^95; sums of weighted values overflow where more
+ * than 65536 positions share the weight of values near bf16's largest); the
+ * softmax weights are rounded to fp16 before they meet the (exact) codes.  A query that sees
  * nothing gives 0 (so do queries before position 0, where n_q >
  * seq_lens[b]).  A length out of range sets BGTQ_DEVERR_SEQ_LEN and counts
  * as 0; a page id outside the pool sets BGTQ_DEVERR_PAGE and page 0 is read.

@@ -36,6 +36,11 @@ constexpr int kStep = 32;                // positions a warp takes at once: half
 constexpr int kStepBytes = kStep * 128;
 constexpr int kByteWaitLimit = 1 << 20;  // polls of up to a microsecond each: about a second
 constexpr float kPShift = 14.f;          // softmax weights are held as 2^14 p (see the weights' comment)
+// Sums of p v are held as 2^-16 of them (2^14 in the weight, 2^-30 with V's
+// scale): they overflow only where more than 2^16 positions share the weight
+// of values near bf16's largest, and the least code of the least scale, 2^-109,
+// stays a normal number.
+constexpr float kVDown = 0x1p-30f, kVUp = 0x1p30f;
 // A unit (one KV head's rows of one sequence) costs a CTA its queries and a
 // merge besides its steps: about as long as this many steps.  Counted when
 // the work is shared out, so that a CTA gets few short sequences.
@@ -825,7 +830,7 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
             }
         }
         // a block that no row sees any of may have any scale, and 0 times it is to be 0
-        vs[0] = fminf(fmaxf(vs[0], 0.f), FLT_MAX);
+        vs[0] = fminf(fmaxf(vs[0], 0.f), FLT_MAX) * kVDown;
         // 4 of the 8 M-tiles (dimension pairs) at a time: half of each 16-byte piece
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -915,7 +920,7 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) sum_l += ls[w * C::kRows + rl] * (mw[w] == mx ? 1.f : ex2(mw[w] - mx));
         m_all[rl] = mx;
-        l_all[rl] = !whole ? sum_l : sum_l == 0.f ? 0.f : 1.f / sum_l;
+        l_all[rl] = !whole ? sum_l : sum_l == 0.f ? 0.f : kVUp / sum_l;
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -1054,7 +1059,7 @@ __global__ __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) void byte_combine_ke
   }
   if constexpr (WARPS == 1) {
     if (!work) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : kVUp / l;
     store2(a, op, acc.x * inv, acc.y * inv);
     store2(a, op + 2, acc.z * inv, acc.w * inv);
   } else {
@@ -1072,7 +1077,7 @@ __global__ __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) void byte_combine_ke
       o = fmaf(f, accs[w][tid], o);
       lt = fmaf(f, ml[w].y, lt);
     }
-    o = lt == 0.f ? 0.f : o / lt;
+    o = lt == 0.f ? 0.f : o / lt * kVUp;
     op += tid - 4 * lane;
     if (a.bf16) {
       const __nv_bfloat16 v = __float2bfloat16_rn(o);

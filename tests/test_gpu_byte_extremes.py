@@ -1,11 +1,12 @@
-"""Attention over the 8-bit cache at the ends of its ranges: scores, scales and biases of any size."""
+"""Attention over the 8-bit cache at the ends of its ranges: scores, scales and biases of any size, values up to the type's
+largest."""
 import numpy as np
 import pytest
 import torch
 
 from packed_decode_attention_b200 import bgtq
 
-from byte_helpers import HALF_STEP, TINY, make, values
+from byte_helpers import HALF_STEP, TINY, check_attention, make, values
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +93,17 @@ def test_slopes_of_the_largest_size(dev, rt):
     v = values(kv.v_codes(), kv.v_scales())[0, 0, 0].reshape(-1, 128)
     for r, at in enumerate((699, 699, 0, 0)):
         assert close(out[0, 0, 0, r], v[at], np.abs(v[at]), rt), r
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("lens,hkv", [([1], 1), ([5, 700], 1), ([4000], 1), ([4000, 1, 3000, 70], 4)])
+def test_values_up_to_the_largest(dev, code, lens, hkv):
+    """Values near bf16's largest: sums over the positions must not overflow where the weighted mean does not."""
+    kv, q, out, sl, _ = make(dev, lens, hkv=hkv, group=4, code=code, rows="bf16")
+    kv.v_scales().fill_(2.0 ** (118 if code == "e4m3" else 120))
+    kv.decode_attn(0, q, sl, out)
+    assert torch.isfinite(out).all()
+    check_attention(kv, q, lens, out)
+    kv.v_scales().fill_(2.0 ** -100)
+    kv.decode_attn(0, q, sl, out)
+    check_attention(kv, q, lens, out)
