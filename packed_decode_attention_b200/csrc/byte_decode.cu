@@ -642,9 +642,13 @@ __global__ __launch_bounds__(Split<NB>::kThreads, 1) void byte_split_kernel(cons
           r.hi = asked.p;
           r.pre = pre;
           r.slope = fminf(fmaxf(asked.slope * kLog2e, -kMaxSlope), kMaxSlope);
-          // distances count from the row's last visible position: its
-          // weights do not change, and the near ones stay exact
-          r.tref = max(asked.lo <= asked.p ? asked.p : -1, pre - 1);
+          // distances count from the row's last visible position, or with a
+          // negative slope its first: its weights do not change, and the
+          // positions that the bias favours keep theirs exact
+          if (asked.slope < 0.f)
+            r.tref = pre > 0 ? 0 : asked.lo;
+          else
+            r.tref = max(asked.lo <= asked.p ? asked.p : -1, pre - 1);
           r.out = asked.out;
         }
         row_info[rl] = r;

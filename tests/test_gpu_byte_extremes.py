@@ -1,9 +1,10 @@
 """Attention over the 8-bit cache at the ends of its ranges: scores, scales and biases of any size, values up to the type's
-largest."""
+largest, biases that grow with the distance."""
 import numpy as np
 import pytest
 import torch
 
+from oracle import byte_cache as bc
 from packed_decode_attention_b200 import bgtq
 
 from byte_helpers import HALF_STEP, TINY, check_attention, make, values
@@ -107,3 +108,38 @@ def test_values_up_to_the_largest(dev, code, lens, hkv):
     kv.v_scales().fill_(2.0 ** -100)
     kv.decode_attn(0, q, sl, out)
     check_attention(kv, q, lens, out)
+
+
+@pytest.mark.parametrize("opt", [{}, {"window": 70000}, {"prefix": 100}, {"prefix": 9, "window": 1000}], ids=str)
+@pytest.mark.parametrize("n_q", [1, 3])
+def test_negative_slopes_keep_the_far_positions(dev, opt, n_q):
+    """With a negative slope the farthest positions weigh most: the bias must be exact there, however far they are.
+
+    The error allowed is byte_helpers.expect's, with the bias of each position counted from the heaviest one
+    (2^-22 of it) and weighed by the position's own weight."""
+    n = 1 << 17
+    kv, q, out, sl, _ = make(dev, [n], hkv=1, group=4, code="int8", n_q=n_q, rows="fp16")
+    slopes = [-1.0, -0.3, -2.0 ** -12, 0.25]
+    dopt = dict(opt)
+    if "prefix" in opt:
+        dopt["prefix"] = i32([opt["prefix"]], dev)
+    kv.decode_attn(0, q, sl, out, slopes=torch.tensor(slopes, device=dev), **dopt)
+    k = values(kv.k_codes(), kv.k_scales())[0, 0, 0].reshape(-1, 128)
+    v = values(kv.v_codes(), kv.v_scales())[0, 0, 0].reshape(-1, 128)
+    for i in range(n_q):
+        see = bc.visible(n, n_q, i, opt.get("window", 0), opt.get("prefix", 0))
+        t = np.arange(n)[see]
+        for r, slope in enumerate(torch.tensor(slopes).double().tolist()):
+            qr = q[0, 0, i, r].double().cpu().numpy()
+            x = k[see] @ qr / np.sqrt(128)
+            s = (np.abs(k[see]) @ np.abs(qr)).max() / np.sqrt(128)
+            bias = slope * (t - (t.min() if slope < 0 else t.max()))      # <= 0
+            w = np.exp(x + bias - (x + bias).max())
+            w /= w.sum()
+            want = w @ v[see]
+            d = s * 2.0 ** -16 + s * 2e-6 + (s + np.abs(bias)) * 2.0 ** -22
+            allowed = (w * (2 * HALF_STEP["fp16"] + 2 * d + 2 * (w @ d) + 2.0 ** -20)) @ np.abs(v[see])
+            allowed = allowed + 2.0 ** -39 * np.abs(v[see]).sum(axis=0)
+            got = out[0, 0, i, r].double().cpu().numpy()
+            allowed = allowed + HALF_STEP["fp16"] * (np.abs(want) + allowed) + TINY["fp16"]
+            assert np.all(np.abs(got - want) <= allowed), (i, r, np.abs(got - want).max(), allowed.min())
