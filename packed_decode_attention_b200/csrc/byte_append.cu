@@ -151,6 +151,7 @@ __global__ __launch_bounds__(kAppThreads, 6) void byte_append_kernel(ByteShape s
     if (tid == 0) atomicOr(err, kErrArg);
     return;
   }
+  if (count == 0) return;  // wherever the sequence stands
   const int64_t past = static_cast<int64_t>(start) + count;
   if (past > sh.capacity && tid == 0) atomicOr(err, kErrCapacity);
   const int end = static_cast<int>(min(past, sh.capacity));  // at most 2^30; slots are fewer than 2^25
