@@ -510,7 +510,8 @@ int bgtq_byte_create(const bgtq_byte_config* cfg, void* d_cache, size_t cache_by
  * (round(code 2^(e_old - e)), ties to even).  New codes are round(x 2^-e),
  * ties to even; the scale is 2^e.  Infinities become the largest code and
  * NaN 0, with BGTQ_DEVERR_NONFINITE.
- *   d_k, d_v   fp16 or bf16 [layer_count][batch][n][n_kv_heads][128]
+ *   d_k, d_v   fp16 or bf16 [layer_count][batch][n][n_kv_heads][128]; n = 0
+ *              appends nothing (they may then be NULL)
  *   d_start    int32 [batch]
  *   d_count    int32 [batch], 0..n
  * Positions at or past the capacity are skipped and set

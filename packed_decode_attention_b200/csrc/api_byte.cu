@@ -203,7 +203,7 @@ int bgtq_byte_create(const bgtq_byte_config* cfg, void* d_cache, size_t cache_by
 
 int bgtq_byte_append(bgtq_state* st, int32_t layer, int32_t layer_count, const void* d_k, const void* d_v,
                      const int32_t* d_start, const int32_t* d_count, int32_t batch, int32_t n, void* stream) {
-  if (!st || !d_k || !d_v || !d_start || !d_count) return BGTQ_ERR_NULL;
+  if (!st || (n != 0 && (!d_k || !d_v)) || !d_start || !d_count) return BGTQ_ERR_NULL;
   const int v = check_byte_call(st, layer, layer_count, batch);
   if (v != BGTQ_OK) return v;
   if (n < 0 || n > (1 << 30) / 64) return BGTQ_ERR_INVALID_ARG;
