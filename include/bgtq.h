@@ -506,7 +506,8 @@ int bgtq_byte_create(const bgtq_byte_config* cfg, void* d_cache, size_t cache_by
  * = the least integer >= -100 with a <= Qmax 2^e_new.  A call that writes the
  * block's first position starts the block anew: e = e_new, and its other
  * positions keep bytes that mean nothing until they are written.  Otherwise e
- * = max(e_old, e_new); where e grew, the block's other codes are rescaled
+ * = max(e_old, e_new), e_old = -100 where the block's scale is no power of two
+ * (a buffer never written; a recycled page's scale is one); where e grew, the block's other codes are rescaled
  * (round(code 2^(e_old - e)), ties to even).  New codes are round(x 2^-e),
  * ties to even; the scale is 2^e.  Infinities become the largest code and
  * NaN 0, with BGTQ_DEVERR_NONFINITE.

@@ -229,8 +229,9 @@ __global__ __launch_bounds__(kAppThreads, 6) void byte_append_kernel(ByteShape s
   int grow = 0;  // e - e_old where the block's other codes are to be rescaled
   if (lo > 0) {
     // a block nothing was written to has no power of two in its place: as the least scale
-    int e_old = static_cast<int>(__float_as_uint(old_scale) >> 23) - 127;
-    if (!(old_scale > 0.f) || e_old < kByteMinExp || e_old > 127) e_old = kByteMinExp;
+    const uint32_t bits = __float_as_uint(old_scale);
+    int e_old = static_cast<int>(bits >> 23 & 255) - 127;
+    if ((bits & 0x807FFFFFu) != 0 || e_old < kByteMinExp || e_old > 127) e_old = kByteMinExp;
     if (e > e_old) grow = e - e_old;
     else e = e_old;
   }

@@ -1,7 +1,9 @@
-"""Appends of nothing to the 8-bit cache."""
+"""Appends of nothing to the 8-bit cache, and into blocks whose scale was never written."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import byte_cache as bc
 from packed_decode_attention_b200 import bgtq
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +46,22 @@ def test_a_call_of_no_rows(dev):
     with pytest.raises(bgtq.BgtqError) as e:
         bgtq.bgtq_byte_append(kv.state, 0, 1, None, None, i32([0], dev), i32([0], dev), 1, 1)
     assert e.value.status == -2
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_a_scale_that_is_no_power_of_two_is_none(dev, code):
+    """A block that starts in its middle, in a buffer that held something else before."""
+    cfg = bgtq.ByteConfig(n_layers=1, n_kv_heads=1, n_q_heads=1, max_batch=1, capacity_tokens=64, code=code)
+    kv = bgtq.ByteKVCache(cfg, dev)
+    k = torch.randn((1, 1, 20, 1, 128), device=dev).half()
+    vals, exps = np.zeros((1, 64, 128)), np.full(1, bc.E_MIN)
+    bc.append(vals, exps, k[0, 0, :, 0].double().cpu().numpy(), 7, 64, code)
+    inf = float("inf")
+    for was in (0.0, 3e20, 1.5 * 2.0 ** 60, 2.0 ** 60 + 2.0 ** 37, -2.0 ** 60, 2.0 ** -101, 2.0 ** -140, inf, -inf, float("nan")):
+        kv.cache.zero_()
+        for s in (kv.k_scales(), kv.v_scales()):
+            s.fill_(was)
+        kv.append(0, k, k, i32([7], dev), i32([20], dev))
+        assert kv.v_scales().item() == kv.k_scales().item() == 2.0 ** exps[0], was
+        assert np.array_equal(kv.k_codes().double().cpu().numpy()[0, 0, 0, 0, 7:27], vals[0, 7:27]), was
+    assert kv.device_error() == 0
