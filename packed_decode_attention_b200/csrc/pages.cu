@@ -131,6 +131,7 @@ __global__ __launch_bounds__(kPlanThreads, 1) void plan_kernel(const __grid_cons
         row = -1;
       }
       len = row < 0 ? 0 : checked_len(a, a.lens[row]);
+      if (row != b) checked_len(a, a.lens[b]);  // for its flag
       part = len;
     } else {
       part = checked_len(a, a.lens[b]);
@@ -437,6 +438,7 @@ __global__ __launch_bounds__(kSmallThreads, 1) void small_plan_kernel(const __gr
         row = -1;
       }
       len = row < 0 ? 0 : checked_len(a, was[row]);
+      if (row != b) checked_len(a, was[b]);  // for its flag
       row_v[b] = row;
     } else {
       const int part = checked_len(a, was[b]);
