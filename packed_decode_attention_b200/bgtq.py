@@ -612,6 +612,9 @@ def rope_axes(q, k, pos, axis, base, q_out=None, k_out=None, pairing=0):
     return q_out, k_out
 
 
+_LATER = object()   # a context that is made when it is first needed
+
+
 class _Pages:
     """The page operations of a paged cache (include/bgtq.h: rows' block table
     int32 [batch, ceil(capacity / 64)], refs int32 [pages], lens int32 [batch],
@@ -620,18 +623,28 @@ class _Pages:
 
     page_scratch = None
     # what the compiled checks compare tensors with; a call whose arguments they
-    # do not pass goes through the checks here, which say what is wrong
+    # do not pass goes through the checks here, which say what is wrong (None: every call)
     _ctx = None
+
+    def _make_scratch(self):
+        import torch
+        if self.cfg.page_pool_tiles > 0:
+            self.page_scratch = torch.empty(bgtq_page_scratch_bytes(self.state), dtype=torch.uint8, device=self.device)
 
     def _make_context(self, rows):
         import torch
         c = self.cfg
-        if c.page_pool_tiles > 0:
-            self.page_scratch = torch.empty(bgtq_page_scratch_bytes(self.state), dtype=torch.uint8, device=self.device)
         self._fast = marshal()
         self._ctx = self._fast.context(self.device, self.device.index, rows, torch.int32, torch.float32, c.n_kv_heads,
                                        c.n_q_heads, (c.capacity_tokens + TILE - 1) // TILE, c.page_pool_tiles,
                                        0 if self.page_scratch is None else self.page_scratch.data_ptr())
+
+    def _context(self):
+        """The context of a page operation; a packed cache makes its own with the first."""
+        if self._ctx is _LATER:
+            import torch
+            self._make_context(torch.float16)
+        return self._ctx
 
     def _through(self, status):
         """Whether a compiled call was made (None: it was not); its error, if any, is raised."""
@@ -651,7 +664,7 @@ class _Pages:
 
     def copy_pages(self, src, dst):
         """Page src[i] to dst[i] (int32 [n]); no page twice in dst or in both lists."""
-        if self._ctx is not None and self._through(self._fast.copy_pages(self._ctx, self.state, src, dst)):
+        if self._context() is not None and self._through(self._fast.copy_pages(self._ctx, self.state, src, dst)):
             return
         import torch
         _expect(src, "src", (None,), torch.int32, self.device)
@@ -662,7 +675,7 @@ class _Pages:
     def fork_sequences(self, parent, table, refs, lens, table_out, refs_out, lens_out):
         """Row b becomes a fork of row parent[b] (-1: empty): whole pages shared, partly filled ones copied for
         every holder but one.  refs_out may be refs, lens_out lens; table_out is another table."""
-        if self._ctx is not None and self._through(self._fast.fork_sequences(
+        if self._context() is not None and self._through(self._fast.fork_sequences(
                 self._ctx, self.state, parent, table, refs, lens, table_out, refs_out, lens_out)):
             return
         import torch
@@ -677,7 +690,7 @@ class _Pages:
         """Row b from lens[b] to new_lens[b] positions: pages given back (0: all) or taken, a shared last page copied
         before it is written.  table and refs change in place; lens_out: the lengths granted (may be lens or
         new_lens)."""
-        if self._ctx is not None and self._through(self._fast.resize_sequences(
+        if self._context() is not None and self._through(self._fast.resize_sequences(
                 self._ctx, self.state, table, refs, lens, new_lens, lens_out)):
             return
         import torch
@@ -689,7 +702,7 @@ class _Pages:
     def compact_pages(self, table, refs, lens, table_out, refs_out, page_map, n_live):
         """Live pages (refs > 0) move to ids 0 .. n_live - 1.  page_map int32 [pages]: new ids, -1 for free ones;
         n_live int32 [1].  table_out may be table, refs_out refs."""
-        if self._ctx is not None and self._through(self._fast.compact_pages(
+        if self._context() is not None and self._through(self._fast.compact_pages(
                 self._ctx, self.state, table, refs, lens, table_out, refs_out, page_map, n_live)):
             return
         import torch
@@ -714,7 +727,8 @@ class PackedKVCache(_Pages):
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         self.state = bgtq_create(cfg, self.cache, self.cache_bytes, self.workspace, self.workspace_bytes)
         self.offsets = bgtq_cache_offsets(self.state)
-        self._make_context(torch.float16)
+        self._make_scratch()
+        self._ctx = _LATER   # the packed cache's own calls do not need the compiled checks
 
     def close(self):
         if getattr(self, "state", None):
@@ -955,6 +969,7 @@ class ByteKVCache(_Pages):
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         self.state = bgtq_byte_create(cfg, self.cache, self.cache_bytes, self.workspace, self.workspace_bytes)
         self.offsets = bgtq_cache_offsets(self.state)
+        self._make_scratch()
         self._make_context(self.row_dtype)
 
     def close(self):
