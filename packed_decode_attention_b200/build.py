@@ -1,6 +1,7 @@
 """Builds the in-tree shared library libbgtq.so for sm_100a with nvcc, and _marshal.so (the Python binding's checks and
 calls of the serving operators), which links to it."""
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -35,11 +36,19 @@ def up_to_date():
 
 
 def build_marshal(force=False, verbose=False):
+    """Builds _marshal.so; None, with a word on stderr, where Python's headers or a C compiler are missing (the packed
+    cache does without it; the serving operators then say what to build)."""
     src, header = os.path.join(PKG, "csrc", "marshal.c"), os.path.join(ROOT, "include", "bgtq.h")
     if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= max(map(os.path.getmtime, (src, header))):
         return MARSHAL
-    cmd = [os.environ.get("CC", "gcc"), "-shared", "-fPIC", "-O2", "-std=c11", "-Wall", "-I",
-           sysconfig.get_paths()["include"], "-o", MARSHAL, src, "-L", PKG, "-lbgtq", "-Wl,-rpath,$ORIGIN"]
+    cc, include = os.environ.get("CC", "gcc"), sysconfig.get_paths()["include"]
+    missing = ([] if os.path.exists(os.path.join(include, "Python.h")) else [os.path.join(include, "Python.h")]) + (
+        [] if shutil.which(cc.split()[0]) else [cc])
+    if missing:
+        print(f"_marshal.so not built: {', '.join(missing)} not found", file=sys.stderr)
+        return None
+    cmd = cc.split() + ["-shared", "-fPIC", "-O2", "-std=c11", "-Wall", "-I", include, "-o", MARSHAL, src, "-L", PKG,
+                        "-lbgtq", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
