@@ -167,10 +167,20 @@ static int stream_at(long index, void** out) {
   return r;
 }
 
+/* The library call, other threads running meanwhile: a launch waits where the
+ * queue of launches is full. */
+#define RELEASED(call)       \
+  do {                       \
+    Py_BEGIN_ALLOW_THREADS   \
+    status = (call);         \
+    Py_END_ALLOW_THREADS     \
+  } while (0)
+
 static const Ctx* ctx_arg(PyObject* x) { return PyCapsule_GetPointer(x, kCtx); }
 
 /* append(ctx, state, layer, layer_count, k, v, start, count) */
 static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int status;
   bgtq_state* st;
   int32_t layer, layers;
   void *k, *v, *start, *count, *stream;
@@ -181,11 +191,13 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (tensor(a[4], c->rows, c->device, 5, s, &k) || tensor(a[5], c->rows, c->device, 5, s, &v) ||
       row_tensor(c, a[6], s[1], &start) || row_tensor(c, a[7], s[1], &count) || stream_at(c->index, &stream))
     return not_here();
-  return PyLong_FromLong(bgtq_byte_append(st, layer, layers, k, v, start, count, (int32_t)s[1], (int32_t)s[2], stream));
+  RELEASED(bgtq_byte_append(st, layer, layers, k, v, start, count, (int32_t)s[1], (int32_t)s[2], stream));
+  return PyLong_FromLong(status);
 }
 
 /* decode_attn(ctx, state, layer, layer_count, q, seq_lens, out, scale, softcap, slopes, window, prefix, doc_start) */
 static PyObject* decode_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int status;
   bgtq_state* st;
   int32_t layer, layers;
   void *q, *lens, *out, *slopes = NULL, *prefix = NULL, *docs = NULL, *stream;
@@ -212,12 +224,13 @@ static PyObject* decode_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   score.d_slopes = slopes;
   score.d_prefix = prefix;
   score.d_doc_start = docs;
-  return PyLong_FromLong(
-      bgtq_byte_decode_attn(st, layer, layers, q, lens, (int32_t)s[1], (int32_t)s[2], &score, out, stream));
+  RELEASED(bgtq_byte_decode_attn(st, layer, layers, q, lens, (int32_t)s[1], (int32_t)s[2], &score, out, stream));
+  return PyLong_FromLong(status);
 }
 
 /* copy_pages(ctx, state, src, dst) */
 static PyObject* copy_pages(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int status;
   bgtq_state* st;
   void *src, *dst, *stream;
   int64_t s[1] = {-1};
@@ -227,11 +240,13 @@ static PyObject* copy_pages(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       tensor(a[3], c->i32, c->device, 1, s, &dst) || stream_at(c->index, &stream))
     return not_here();
   if (s[0] == 0) return PyLong_FromLong(0);
-  return PyLong_FromLong(bgtq_copy_pages(st, src, dst, (int32_t)s[0], stream));
+  RELEASED(bgtq_copy_pages(st, src, dst, (int32_t)s[0], stream));
+  return PyLong_FromLong(status);
 }
 
 /* fork_sequences(ctx, state, parent, table, refs, lens, table_out, refs_out, lens_out) */
 static PyObject* fork_sequences(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int status;
   bgtq_state* st;
   void *parent, *table, *refs, *lens, *table_out, *refs_out, *lens_out, *stream;
   int64_t s[1] = {-1};
@@ -242,12 +257,13 @@ static PyObject* fork_sequences(PyObject* self, PyObject* const* a, Py_ssize_t n
       table_tensor(c, a[6], s[0], &table_out) || row_tensor(c, a[7], c->pages, &refs_out) ||
       row_tensor(c, a[8], s[0], &lens_out) || stream_at(c->index, &stream))
     return not_here();
-  return PyLong_FromLong(bgtq_fork_sequences(st, parent, table, refs, lens, (int32_t)s[0], table_out, refs_out, lens_out,
-                                             c->scratch, stream));
+  RELEASED(bgtq_fork_sequences(st, parent, table, refs, lens, (int32_t)s[0], table_out, refs_out, lens_out, c->scratch, stream));
+  return PyLong_FromLong(status);
 }
 
 /* resize_sequences(ctx, state, table, refs, lens, new_lens, lens_out) */
 static PyObject* resize_sequences(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int status;
   bgtq_state* st;
   void *table, *refs, *lens, *new_lens, *lens_out, *stream;
   int64_t s[1] = {-1};
@@ -257,12 +273,13 @@ static PyObject* resize_sequences(PyObject* self, PyObject* const* a, Py_ssize_t
       table_tensor(c, a[2], s[0], &table) || row_tensor(c, a[3], c->pages, &refs) ||
       row_tensor(c, a[5], s[0], &new_lens) || row_tensor(c, a[6], s[0], &lens_out) || stream_at(c->index, &stream))
     return not_here();
-  return PyLong_FromLong(
-      bgtq_resize_sequences(st, table, refs, lens, new_lens, (int32_t)s[0], lens_out, c->scratch, stream));
+  RELEASED(bgtq_resize_sequences(st, table, refs, lens, new_lens, (int32_t)s[0], lens_out, c->scratch, stream));
+  return PyLong_FromLong(status);
 }
 
 /* compact_pages(ctx, state, table, refs, lens, table_out, refs_out, page_map, n_live) */
 static PyObject* compact_pages(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int status;
   bgtq_state* st;
   void *table, *refs, *lens, *table_out, *refs_out, *map, *live, *stream;
   int64_t s[1] = {-1};
@@ -273,8 +290,8 @@ static PyObject* compact_pages(PyObject* self, PyObject* const* a, Py_ssize_t n)
       table_tensor(c, a[5], s[0], &table_out) || row_tensor(c, a[6], c->pages, &refs_out) ||
       row_tensor(c, a[7], c->pages, &map) || row_tensor(c, a[8], 1, &live) || stream_at(c->index, &stream))
     return not_here();
-  return PyLong_FromLong(bgtq_compact_pages(st, table, refs, lens, (int32_t)s[0], table_out, refs_out, map, live,
-                                            c->scratch, stream));
+  RELEASED(bgtq_compact_pages(st, table, refs, lens, (int32_t)s[0], table_out, refs_out, map, live, c->scratch, stream));
+  return PyLong_FromLong(status);
 }
 
 /* Rows [tokens, heads, 128], heads contiguous: address and elements from a
@@ -339,8 +356,9 @@ static PyObject* rope_axes(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   cfg.head_dim = 128;
   cfg.dtype = dtype == a[1] ? BGTQ_DTYPE_BFLOAT : BGTQ_DTYPE_HALF;
   cfg.n_axes = (int32_t)ps[0];
-  result = PyLong_FromLong(
-      tokens == 0 ? 0 : bgtq_rope_axes(&cfg, q, sq, k, sk, pos, (int32_t)tokens, q_out, sqo, k_out, sko, stream));
+  int status = 0;
+  if (tokens != 0) RELEASED(bgtq_rope_axes(&cfg, q, sq, k, sk, pos, (int32_t)tokens, q_out, sqo, k_out, sko, stream));
+  result = PyLong_FromLong(status);
 done:
   Py_XDECREF(axis);
   Py_XDECREF(dtype);
