@@ -233,7 +233,8 @@ int bgtq_byte_decode_attn(bgtq_state* st, int32_t layer, int32_t layer_count, co
       return BGTQ_ERR_ALIGNMENT;
     a.cap = static_cast<float>(score->softcap);
     if (score->softcap > 0.0 && a.cap < 1e-30f) return BGTQ_ERR_INVALID_ARG;
-    a.window = score->window;
+    // past the capacity a window hides nothing (and p - window + 1 stays in an int32)
+    a.window = score->window >= st->byte_shape.capacity ? 0 : score->window;
     a.slopes = score->d_slopes;
     a.prefix = score->d_prefix;
     a.doc_start = score->d_doc_start;

@@ -59,3 +59,14 @@ def test_unseen_positions_may_hold_anything(dev, code, group, n_q, case):
             scales[0, b, 0, (~seen.view(-1, 64).any(1)).to(dev)] = float("nan")
     kv.decode_attn(0, q, sl, out, **opt)
     assert torch.equal(out, want) and kv.device_error() == 0
+
+
+def test_the_widest_window(dev):
+    """A window past the capacity, at lengths shorter than the call's queries: as none."""
+    lens = [3, 0, 200]
+    kv, q, out, sl, _ = make(dev, lens, hkv=1, group=2, n_q=16)
+    want = torch.empty_like(q)
+    kv.decode_attn(0, q, sl, want)
+    for window in (200, 2 ** 31 - 1):
+        kv.decode_attn(0, q, sl, out.fill_(1), window=window)
+        assert torch.equal(out, want)
