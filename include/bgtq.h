@@ -109,7 +109,8 @@ enum {
   BGTQ_DEVERR_ARG = 4,         /* encode_append: start < 0 or count < 0 or count > n */
   BGTQ_DEVERR_NONFINITE = 8,   /* allocate: a calibration value is Inf or NaN; byte_append: a row's element is
                                   (stored as the largest code, NaN as 0) */
-  BGTQ_DEVERR_TIMEOUT = 16,    /* decode: a wait for a tile copy gave up (bounded spin) */
+  BGTQ_DEVERR_TIMEOUT = 16,    /* decode: a wait for a tile copy gave up (bounded spin); page operations: a page
+                                  copy's wait did, and pages to be written may hold parts of either content */
   BGTQ_DEVERR_PAGE = 32,       /* paged cache: a block-table entry outside [0, page_pool_tiles) (encode skips the
                                   tile, decode reads page 0 instead, logit MAE skips the tile) */
   BGTQ_DEVERR_POOL = 64        /* fork_sequences, resize_sequences: no free page was left for some row */
@@ -556,10 +557,11 @@ typedef struct {
  * only bf16 rows reach, may count as less than it is, but past 2^57; a
  * slope past 2^95 counts as 2^95; sums of weighted values overflow where more
  * than 65536 positions share the weight of values near bf16's largest); the
- * softmax weights are rounded to fp16 before they meet the (exact) codes.  A query that sees
- * nothing gives 0 (so do queries before position 0, where n_q >
- * seq_lens[b]).  A length out of range sets BGTQ_DEVERR_SEQ_LEN and counts
- * as 0; a page id outside the pool sets BGTQ_DEVERR_PAGE and page 0 is read.
+ * softmax weights are rounded to fp16 before they meet the (exact) codes.  A
+ * query that sees nothing gives 0; one before position 0 (where n_q >
+ * seq_lens[b]) sees the prefix alone.  A length out of range sets
+ * BGTQ_DEVERR_SEQ_LEN and counts as 0; a page id outside the pool sets
+ * BGTQ_DEVERR_PAGE and page 0 is read.
  * Results do not depend on the batch's other sequences beyond the order of
  * floating-point sums, and are the same each time.  Uses the workspace: two
  * such calls on one state must not overlap on the GPU (captured graphs that

@@ -958,6 +958,10 @@ class ByteKVCache(_Pages):
                                     capacity_tokens=131072, code="int8", rows="bf16"), "cuda")
         kv.append(l, k, v, start, count)              # prefill, then each step's rows
         kv.decode_attn(l, q, seq_lens, out)           # q [1, batch, n_q, n_q_heads, 128]
+
+    The attention calls of one cache share a workspace, the page operations a
+    scratch buffer: issue them on one stream, or order the streams (captured
+    graphs included).
     """
 
     def __init__(self, cfg, device="cuda"):
@@ -1044,7 +1048,7 @@ class ByteKVCache(_Pages):
         None: 1/sqrt(128)).  softcap c: scores become c tanh(x / c).  slopes fp32
         [Hq]: slope * distance is taken off.  window: positions a query sees,
         its own included.  prefix int32 [batch]: positions below it are seen by
-        every query.  doc_start int32 [batch, n_q]: the first position of each
+        every query, also one before position 0 (n_q > seq_lens).  doc_start int32 [batch, n_q]: the first position of each
         query's document.
         """
         if self._ctx is not None and self._through(self._fast.decode_attn(
