@@ -490,8 +490,9 @@ typedef struct {
 } bgtq_byte_config;
 
 /* Bytes of the two caller-owned device buffers.  A config of 2^31 - 64 or
- * more positions over all layers, heads and sequences (or pages) is
- * rejected with BGTQ_ERR_INVALID_ARG.  SYNC (host only). */
+ * more positions over all layers, heads and sequences (or pages), or of more
+ * than 2^24 query rows a sequence (n_q_heads x max_q_tokens), is rejected with
+ * BGTQ_ERR_INVALID_ARG.  SYNC (host only). */
 int bgtq_byte_required_bytes(const bgtq_byte_config* cfg, size_t* cache_bytes, size_t* workspace_bytes);
 
 /* Creates a state over caller buffers (256-byte aligned, at least the

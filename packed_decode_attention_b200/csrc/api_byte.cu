@@ -47,6 +47,8 @@ int validate(const bgtq_byte_config* c) {
   if (c->capacity_tokens < 1 || c->capacity_tokens > (int64_t(1) << 30)) return BGTQ_ERR_INVALID_ARG;
   // the codes' rows of 128 bytes are addressed by an int32 coordinate
   if (slots_estimate(c) * bgtq::kByteBlock > 2147483648.0 - bgtq::kByteBlock) return BGTQ_ERR_INVALID_ARG;
+  // a sequence's query and output elements are addressed by an int32 offset
+  if (double(c->n_q_heads) * c->max_q_tokens * bgtq::kD > 2147483648.0) return BGTQ_ERR_INVALID_ARG;
   // the workspace's places for each unit of a call
   if (double(c->n_layers) * c->n_q_heads * c->max_q_tokens * double(c->max_batch) > 1125899906842624.0)  // 2^50
     return BGTQ_ERR_INVALID_ARG;
