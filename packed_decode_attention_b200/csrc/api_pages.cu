@@ -150,12 +150,12 @@ int bgtq_resize_sequences(bgtq_state* st, int32_t* d_table, int32_t* d_refs, con
   if (!st || !d_table || !d_refs || !d_lens || !d_new_lens || !d_lens_out || !d_scratch) return BGTQ_ERR_NULL;
   if (const int v = check_paged(st, batch)) return v;
   const int64_t pool = 4 * int64_t(st->cache.n_pages), rows = 4 * int64_t(batch), tb = table_bytes(st, batch);
-  // lens_out may be either of the lengths
+  // lens_out may be either of the lengths, or both where they are one
   const bool is_new = d_lens_out == d_new_lens;
   const Range in[2] = {{is_new ? d_new_lens : d_lens, rows}, {is_new ? d_lens : d_new_lens, rows}};
   const Range out[4] = {{d_table, tb}, {d_refs, pool}, {d_lens_out, rows}, scratch_range(st, d_scratch)};
   const int twin[4] = {-1, -1, 0, -1};
-  if (const int v = check_ranges(in, 2, out, 4, twin)) return v;
+  if (const int v = check_ranges(in, d_lens == d_new_lens ? 1 : 2, out, 4, twin)) return v;
   bgtq::PagePlanArgs a = plan_args(st, batch, d_scratch);
   a.table = d_table;
   a.refs = d_refs;

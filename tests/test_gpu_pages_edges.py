@@ -1,4 +1,4 @@
-"""Forks of rows whose lengths are out of range."""
+"""Forks of rows whose lengths are out of range; lengths that are input and output at once."""
 import pytest
 import torch
 
@@ -35,3 +35,16 @@ def test_fork_flags_lengths_nobody_forks_from(dev, batch, pool):
         parent[1] = 1                                   # forked from by itself: the same
         kv.fork_sequences(i32(parent, dev), tb, refs, ln, out, r, n)
         assert kv.device_error() == bgtq.DEVERR_SEQ_LEN and n[1].item() == 0
+
+
+@pytest.mark.parametrize("pool", [6, 9000])
+def test_resize_to_the_lengths_it_has(dev, pool):
+    """One array as the lengths, the new lengths and the lengths granted: nothing changes."""
+    kv = bgtq.ByteKVCache(bgtq.ByteConfig(1, 1, 1, 3, 128, page_pool_tiles=pool), dev)
+    table, refs, lens = i32([[0, 1], [2, -1], [0, -1]], dev), i32([2, 1, 1] + [0] * (pool - 3), dev), i32([100, 7, 64], dev)
+    before = [t.clone() for t in (table, refs, lens)]
+    kv.resize_sequences(table, refs, lens, lens, lens)
+    assert all(torch.equal(a, b) for a, b in zip((table, refs, lens), before)) and kv.device_error() == 0
+    with pytest.raises(bgtq.BgtqError) as e:
+        kv.resize_sequences(table, refs, table[:, 0].contiguous(), lens, refs[:3])
+    assert e.value.status == -1
