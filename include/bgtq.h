@@ -103,16 +103,18 @@ enum {
 
 /* Device error flag bits, reported by bgtq_get_device_error. */
 enum {
-  BGTQ_DEVERR_CAPACITY = 1,    /* encode_append: start + count > capacity (rows skipped) */
+  BGTQ_DEVERR_CAPACITY = 1,    /* encode_append, byte_append: start + count > capacity (rows skipped) */
   BGTQ_DEVERR_SEQ_LEN = 2,     /* decode: a seq_len < 0 or > capacity (sequence skipped, output 0), or a pos_lo /
-                                  buf_count out of range (clamped) */
-  BGTQ_DEVERR_ARG = 4,         /* encode_append: start < 0 or count < 0 or count > n */
+                                  buf_count out of range (clamped); page operations: a length out of range */
+  BGTQ_DEVERR_ARG = 4,         /* encode_append, byte_append: start < 0 or count < 0 or count > n; fork_sequences: a
+                                  parent out of range */
   BGTQ_DEVERR_NONFINITE = 8,   /* allocate: a calibration value is Inf or NaN; byte_append: a row's element is
                                   (stored as the largest code, NaN as 0) */
   BGTQ_DEVERR_TIMEOUT = 16,    /* decode: a wait for a tile copy gave up (bounded spin); page operations: a page
                                   copy's wait did, and pages to be written may hold parts of either content */
-  BGTQ_DEVERR_PAGE = 32,       /* paged cache: a block-table entry outside [0, page_pool_tiles) (encode skips the
-                                  tile, decode reads page 0 instead, logit MAE skips the tile) */
+  BGTQ_DEVERR_PAGE = 32,       /* paged cache: a block-table entry outside [0, page_pool_tiles) (encode and byte_append
+                                  skip the tile, decode reads page 0 instead, logit MAE skips the tile); page
+                                  operations: a page id in use outside it, or one that is free (compact_pages) */
   BGTQ_DEVERR_POOL = 64        /* fork_sequences, resize_sequences: no free page was left for some row */
 };
 

@@ -1048,8 +1048,8 @@ class ByteKVCache(_Pages):
         None: 1/sqrt(128)).  softcap c: scores become c tanh(x / c).  slopes fp32
         [Hq]: slope * distance is taken off.  window: positions a query sees,
         its own included.  prefix int32 [batch]: positions below it are seen by
-        every query, also one before position 0 (n_q > seq_lens).  doc_start int32 [batch, n_q]: the first position of each
-        query's document.
+        every query, also one before position 0 (n_q > seq_lens).  doc_start
+        int32 [batch, n_q]: the first position of each query's document.
         """
         if self._ctx is not None and self._through(self._fast.decode_attn(
                 self._ctx, self.state, layer, layer_count, q, seq_lens, out, scale, softcap, slopes, window, prefix,

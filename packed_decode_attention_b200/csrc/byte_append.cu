@@ -128,8 +128,8 @@ struct Divisor {
 // 256 bytes are one warp half's load.  Magnitudes are compared as packed
 // 16-bit integers, and finite rows of an ordinary size are converted two
 // elements at a time; other rows take the path through fp32, element by
-// element (all rows that way: 52 us where this takes 33).  Bound by HBM, 2
-// bytes read and 1 written an element: 32768 rows of 8 heads take 33.4 us, 92 %
+// element (all rows that way: 52 us where this takes 33.5).  Bound by HBM, 2
+// bytes read and 1 written an element: 32768 rows of 8 heads take 33.5 us, 92 %
 // of the copy rate, at 6 CTAs an SM (4: 36.4).
 template <bool BF16, int CODE>
 __global__ __launch_bounds__(kAppThreads, 6) void byte_append_kernel(ByteShape sh, ByteCacheDev cache,

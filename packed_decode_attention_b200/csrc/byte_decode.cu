@@ -12,10 +12,10 @@
 // the parts of units that more than one CTA attended.
 //
 // Bound by HBM where there is enough to read: a ragged batch of 16 x 16K to 32K
-// positions, 4 KV heads (429 MB) takes 82 us, 80 % of the copy rate, of which
+// positions, 4 KV heads (429 MB) takes 83 us, 79 % of the copy rate, of which
 // about 10 us are not the pass over the codes: a call with nothing to attend
 // takes 2.4 to 3.3 us, the way to the first codes 4, the merge 2, the join 3.
-// One layer of 8 KV heads at 32K takes 23.4 us (67 MB, 44 %): there those count.
+// One layer of 8 KV heads at 32K takes 23.3 us (67 MB, 44 %): there those count.
 //
 // The products run on mma.sync, not tcgen05: its 128-row operand would be filled
 // by 1 to 16 query rows or, with the codes as that operand, leave a row's
@@ -343,10 +343,10 @@ __device__ __forceinline__ void start_of(int64_t off, int64_t left, int pad, Cur
 }
 
 // NB blocks of 8 query rows.  One: 12 warps of 168 registers; two, with twice
-// the accumulators: 8 warps of 255 (12 of 168 spill: 39 us where these take 28).
+// the accumulators: 8 warps of 255 (12 of 168 spill: 39 us where these take 28.5).
 // More than 16 rows take several passes.  (One block, the ragged batch: 16
 // warps of 128 registers spill, 99 us; 8 of 221 in steps of 64 positions, 86; 12
-// are 82.)  Two pairs of buffers a warp (a step's K and V) keep 192 or 128 KB an
+// are 83.)  Two pairs of buffers a warp (a step's K and V) keep 192 or 128 KB an
 // SM on their way, where 64 reach the read rate (three pairs for two blocks
 // were 5 % slower).
 template <int NB>
