@@ -24,7 +24,7 @@ def make(kind, dev, pool, batch=1, cap=64):
     """A paged cache of 37 x 4 (layer, head) pairs whose every byte is random, and the warps that a copy runs on it."""
     common = dict(n_layers=37, n_kv_heads=4, n_q_heads=4, max_batch=batch, capacity_tokens=cap, page_pool_tiles=pool)
     if kind == "packed":
-        kv, slot = bgtq.PackedKVCache(bgtq.Config(k_avg_bits=3, v_avg_bits=2, **common), dev), 3072 + 512 + 2048 + 128
+        kv, slot = bgtq.PackedKVCache(bgtq.Config(k_avg_bits=3, v_avg_bits=2, **common), dev), 1024 * 5 + 512 + 128
     else:
         kv, slot = bgtq.ByteKVCache(bgtq.ByteConfig(code=kind, **common), dev), 16384
     g = torch.Generator(device=dev)
